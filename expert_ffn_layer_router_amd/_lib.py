@@ -21,6 +21,10 @@ MOE_ERR_BAD_STATE = 5
 MOE_FLAG_BAD_SLOT = 0x1
 MOE_NUM_STAGES = 5
 STAGE_NAMES = ("router", "regroup", "gate_up", "down", "combine")
+MOE_TYPE_BF16, MOE_TYPE_FP16, MOE_TYPE_FP32 = 0, 1, 2
+MOE_ACT_SILU, MOE_ACT_GELU = 0, 1
+MOE_OPS = {"int8_product": 0, "int8_gated": 1, "expert_product": 2, "expert_product_backward": 3,
+           "gated_product": 4, "gated_product_backward": 5}
 
 
 class MoeConfig(ctypes.Structure):
@@ -38,6 +42,10 @@ class MoeWeights(ctypes.Structure):
 class MoeRouting(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in
                 ("topk_idx", "topk_w", "counts", "offsets", "perm", "inv_perm")]
+
+
+class MoeProduct(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("rows", "n", "k", "groups", "type", "activation")]
 
 
 class MoeError(RuntimeError):
@@ -71,7 +79,8 @@ def load():
                            "`python -m expert_ffn_layer_router_amd.build`")
     lib = ctypes.CDLL(LIB_PATH)
     c_int, vp, sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
-    i32 = ctypes.c_int32
+    i32, i64 = ctypes.c_int32, ctypes.c_int64
+    product = ctypes.POINTER(MoeProduct)
     sig = {
         "moe_create": (c_int, [ctypes.POINTER(MoeConfig), ctypes.POINTER(vp)]),
         "moe_destroy": (None, [vp]),
@@ -94,6 +103,15 @@ def load():
         "moe_set_stage_timing": (c_int, [vp, i32]),
         "moe_stage_times": (c_int, [vp, ctypes.POINTER(ctypes.c_float), i32, ctypes.POINTER(i32)]),
         "moe_hbm_read_probe": (c_int, [vp, sz, vp, i32, vp]),
+        "moe_product_workspace": (c_int, [product, c_int, ctypes.POINTER(sz)]),
+        "moe_quantize_rows": (c_int, [i32, i32, i32, vp, i64, vp, i64, vp, vp]),
+        "moe_int8_product": (c_int, [product, vp, i64, vp, vp, vp, vp, vp, i64, vp, sz, vp]),
+        "moe_int8_gated": (c_int, [product, vp, i64, vp, vp, vp, vp, vp, i64, vp, sz, vp]),
+        "moe_expert_product": (c_int, [product, vp, i64, vp, vp, vp, i64, vp, sz, vp]),
+        "moe_expert_product_backward": (c_int, [product, vp, i64, vp, i64, vp, vp, vp, i64, vp, i32, vp, sz, vp]),
+        "moe_gated_product": (c_int, [product, vp, i64, vp, vp, vp, i64, vp, i64, vp, sz, vp]),
+        "moe_gated_product_backward": (c_int, [product, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i32, vp, sz,
+                                               vp]),
         "moe_status_string": (ctypes.c_char_p, [c_int]),
         "moe_last_error": (ctypes.c_char_p, []),
     }

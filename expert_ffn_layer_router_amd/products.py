@@ -1,0 +1,298 @@
+"""Grouped products of expert feed-forward blocks (include/moe_ops.h): 8-bit
+codes for serving, 16-bit weights forward and backward for training.
+
+Rows of one expert stand together: group e owns rows offsets[e] ..
+offsets[e + 1] - 1 (int32, on the device; `MoeLayer.routing(...)["offsets"]` is
+such an array), and `w[e]` is its weight matrix, [n, k] as in torch.nn.Linear.
+Without `offsets` there is one group of all rows and w may be [n, k].  Rows
+outside every group are not read, and their outputs are left as they were (in
+a result that the call allocates: unspecified).
+
+Row matrices may have any row stride that is a multiple of 8 elements (16 for
+codes); weights, scales and offsets are contiguous.  A call runs on `stream`
+(default: the current stream of the tensors' device) and allocates what it is
+not given there; with `out` and `workspace` given it allocates nothing."""
+
+from __future__ import annotations
+
+import ctypes
+from functools import lru_cache
+
+from . import _lib
+
+ACTIVATIONS = {"silu": _lib.MOE_ACT_SILU, "gelu": _lib.MOE_ACT_GELU}
+
+
+def _torch():
+    import torch
+    return torch
+
+
+@lru_cache(maxsize=None)
+def _types():
+    torch = _torch()
+    return {torch.bfloat16: _lib.MOE_TYPE_BF16, torch.float16: _lib.MOE_TYPE_FP16, torch.float32: _lib.MOE_TYPE_FP32}
+
+
+@lru_cache(maxsize=1024)
+def _shape(op: int, rows: int, n: int, k: int, groups: int, type_: int, act: int):
+    """(the C struct, workspace bytes) of a call: pure host arithmetic of its arguments."""
+    p = _lib.MoeProduct(rows, n, k, groups, type_, act)
+    need = ctypes.c_size_t()
+    _lib.check(_lib.load().moe_product_workspace(ctypes.byref(p), op, ctypes.byref(need)))
+    return p, need.value
+
+
+def product_workspace(op: str, rows: int, n: int, k: int, groups: int = 1, dtype=None, activation=None) -> int:
+    """Bytes of workspace of a call of `op` ("int8_product", "int8_gated", "expert_product",
+    "expert_product_backward", "gated_product" or "gated_product_backward") with this shape."""
+    if op not in _lib.MOE_OPS:
+        raise ValueError(f"op must be one of {sorted(_lib.MOE_OPS)}, not {op!r}")
+    return _shape(_lib.MOE_OPS[op], int(rows), int(n), int(k), int(groups),
+                  _type(dtype or _torch().bfloat16), _act(activation) if "gated" in op else 0)[1]
+
+
+def _type(dtype) -> int:
+    t = _types().get(dtype)
+    if t is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    return t
+
+
+def _act(name) -> int:
+    a = ACTIVATIONS.get(name or "silu")
+    if a is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, not {name!r}")
+    return a
+
+
+class _Call:
+    """Checks the tensors of one call against each other, finds its stream and
+    makes the calling thread's device and stream match while it allocates and
+    enqueues."""
+
+    def __init__(self, first, stream):
+        torch = _torch()
+        self.lib = _lib.load()
+        if not first.is_cuda:
+            raise ValueError("the tensors must be on a GPU")
+        self.device = first.device
+        self._guards = []
+        if torch.cuda.current_device() != self.device.index:
+            self._guards.append(torch.cuda.device(self.device))
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        else:
+            if stream.device != self.device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
+            self._guards.append(torch.cuda.stream(stream))
+        self.stream = ctypes.c_void_p(stream.cuda_stream)
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+
+    def rows(self, name, t, rows, width, dtype):
+        """(pointer, row stride) of a [rows, width] matrix."""
+        self.same_device(name, t)
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+        if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+            raise ValueError(f"{name} must be [{rows}, {width}], not {list(t.shape)}")
+        if t.stride(1) != 1:
+            raise ValueError(f"the values of a row of {name} must be contiguous")
+        return t.data_ptr(), (t.stride(0) if rows > 1 else width)
+
+    def plain(self, name, t, shape, dtype):
+        """Pointer of a contiguous tensor."""
+        self.same_device(name, t)
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def same_device(self, name, t):
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, not on {self.device}")
+
+    def offsets(self, offsets, groups):
+        if offsets is None:
+            return None
+        return self.plain("offsets", offsets, (groups + 1,), _torch().int32)
+
+    def workspace(self, workspace, need):
+        """(pointer, bytes, tensor kept alive until the call returns)."""
+        if workspace is None:
+            if need == 0:
+                return None, 0, None
+            workspace = _torch().empty(need, dtype=_torch().uint8, device=self.device)
+        else:
+            self.same_device("workspace", workspace)
+            if not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+    def result(self, name, out, rows, width, dtype):
+        if out is None:
+            out = _torch().empty((rows, width), dtype=dtype, device=self.device)
+        return (out, *self.rows(name, out, rows, width, dtype))
+
+
+def _weights(w, gated):
+    """(groups, n, k) of w [groups, n (gated: 2n), k] or [n, k]."""
+    if w.dim() not in (2, 3):
+        raise ValueError(f"w must be [groups, n, k] or [n, k], not {list(w.shape)}")
+    groups = w.shape[0] if w.dim() == 3 else 1
+    wide, k = w.shape[-2], w.shape[-1]
+    if gated and wide % 2:
+        raise ValueError(f"w has {wide} rows a group; gate and up rows come in equal numbers")
+    return groups, wide // 2 if gated else wide, k
+
+
+def _matrix_rows(name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, not {list(t.shape)}")
+    return t.shape[0]
+
+
+def quantize_rows(x, codes=None, scale=None, stream=None):
+    """(codes int8 [rows, k], scale fp32 [rows]) of x [rows, k] (bf16 or fp16):
+    scale = max|row| / 127, codes = rint(row / scale) (moe_quantize_rows)."""
+    torch = _torch()
+    rows = _matrix_rows("x", x)
+    k = x.shape[1]
+    with _Call(x, stream) as c:
+        px, ldx = c.rows("x", x, rows, k, x.dtype)
+        codes, pc, ldc = c.result("codes", codes, rows, k, torch.int8)
+        if scale is None:
+            scale = torch.empty(rows, dtype=torch.float32, device=c.device)
+        ps = c.plain("scale", scale, (rows,), torch.float32)
+        _lib.check(c.lib.moe_quantize_rows(rows, k, _type(x.dtype), px, ldx, pc, ldc, ps, c.stream))
+    return codes, scale
+
+
+def _int8(op, codes, scale, w, w_scale, offsets, activation, out, dtype, workspace, stream):
+    torch = _torch()
+    gated = activation is not None
+    rows = _matrix_rows("codes", codes)
+    groups, n, k = _weights(w, gated)
+    if dtype is None:
+        dtype = out.dtype if out is not None else torch.bfloat16
+    with _Call(codes, stream) as c:
+        pc, ldc = c.rows("codes", codes, rows, k, torch.int8)
+        ps = c.plain("scale", scale, (rows,), torch.float32)
+        pw = c.plain("w", w, w.shape, torch.int8)
+        pws = c.plain("w_scale", w_scale, w.shape[:-1], torch.float32)
+        po = c.offsets(offsets, groups)
+        shape, need = _shape(op, rows, n, k, groups, _type(dtype), _act(activation) if gated else 0)
+        out, pout, ldout = c.result("out", out, rows, n, dtype)
+        ws, ws_bytes, _alive = c.workspace(workspace, need)
+        fn = c.lib.moe_int8_gated if gated else c.lib.moe_int8_product
+        _lib.check(fn(ctypes.byref(shape), pc, ldc, ps, pw, pws, po, pout, ldout, ws, ws_bytes, c.stream))
+    return out
+
+
+def int8_product(codes, scale, w, w_scale, offsets=None, out=None, dtype=None, workspace=None, stream=None):
+    """y[r] = scale[r] w_scale[e] * (codes[r] w[e]^T): codes int8 [rows, k], scale fp32 [rows],
+    w int8 [groups, n, k], w_scale fp32 [groups, n]; y [rows, n] bf16 (default), fp16 or fp32."""
+    return _int8(_lib.MOE_OPS["int8_product"], codes, scale, w, w_scale, offsets, None, out, dtype, workspace, stream)
+
+
+def int8_gated(codes, scale, w, w_scale, offsets=None, activation="silu", out=None, dtype=None, workspace=None,
+               stream=None):
+    """h = act(g) * u, (g, u) the int8 product with w int8 [groups, 2n, k] (gate rows, then up rows);
+    h [rows, n] bf16 (default) or fp16."""
+    return _int8(_lib.MOE_OPS["int8_gated"], codes, scale, w, w_scale, offsets, activation or "silu", out, dtype,
+                 workspace, stream)
+
+
+def expert_product(x, w, offsets=None, out=None, workspace=None, stream=None):
+    """y = x w[e]^T: x [rows, k], w [groups, n, k], both bf16 or both fp16; y [rows, n]."""
+    rows = _matrix_rows("x", x)
+    groups, n, k = _weights(w, False)
+    with _Call(x, stream) as c:
+        px, ldx = c.rows("x", x, rows, k, x.dtype)
+        pw = c.plain("w", w, w.shape, x.dtype)
+        po = c.offsets(offsets, groups)
+        shape, need = _shape(_lib.MOE_OPS["expert_product"], rows, n, k, groups, _type(x.dtype), 0)
+        out, pout, ldout = c.result("out", out, rows, n, x.dtype)
+        ws, ws_bytes, _alive = c.workspace(workspace, need)
+        _lib.check(c.lib.moe_expert_product(ctypes.byref(shape), px, ldx, pw, po, pout, ldout, ws, ws_bytes, c.stream))
+    return out
+
+
+def gated_product(x, w, offsets=None, activation="silu", save=False, out=None, gate_up=None, workspace=None,
+                  stream=None):
+    """h = act(g) * u with (g, u) = x w[e]^T: w [groups, 2n, k] (gate rows, then up rows); h [rows, n].
+    With `save` (or a `gate_up` to fill) returns (h, gate_up [rows, 2n]), which the backward pass takes."""
+    rows = _matrix_rows("x", x)
+    groups, n, k = _weights(w, True)
+    save = save or gate_up is not None
+    with _Call(x, stream) as c:
+        px, ldx = c.rows("x", x, rows, k, x.dtype)
+        pw = c.plain("w", w, w.shape, x.dtype)
+        po = c.offsets(offsets, groups)
+        shape, need = _shape(_lib.MOE_OPS["gated_product"], rows, n, k, groups, _type(x.dtype), _act(activation))
+        out, pout, ldout = c.result("out", out, rows, n, x.dtype)
+        pg, ldg = None, 0
+        if save:
+            gate_up, pg, ldg = c.result("gate_up", gate_up, rows, 2 * n, x.dtype)
+        ws, ws_bytes, _alive = c.workspace(workspace, need)
+        _lib.check(c.lib.moe_gated_product(ctypes.byref(shape), px, ldx, pw, po, pout, ldout, pg, ldg, ws, ws_bytes,
+                                           c.stream))
+    return (out, gate_up) if save else out
+
+
+def _backward(name, dy, gate_up, x, w, offsets, activation, need_dx, need_dw, dx, dw, dw_dtype, workspace, stream):
+    torch = _torch()
+    gated = activation is not None
+    rows = _matrix_rows("dh" if gated else "dy", dy)
+    groups, n, k = _weights(w, gated)
+    dtype = dy.dtype
+    need_dx, need_dw = need_dx or dx is not None, need_dw or dw is not None
+    with _Call(dy, stream) as c:
+        py, ldy = c.rows("dh" if gated else "dy", dy, rows, n, dtype)
+        px, ldx = c.rows("x", x, rows, k, dtype)
+        pw = c.plain("w", w, w.shape, dtype)
+        po = c.offsets(offsets, groups)
+        shape, need = _shape(_lib.MOE_OPS[name], rows, n, k, groups, _type(dtype), _act(activation) if gated else 0)
+        pdx, lddx, pdw = None, 0, None
+        if need_dx:
+            dx, pdx, lddx = c.result("dx", dx, rows, k, dtype)
+        if need_dw:
+            if dw is None:
+                dw = torch.empty(w.shape, dtype=dw_dtype or dtype, device=c.device)
+            pdw = c.plain("dw", dw, w.shape, dw_dtype or dw.dtype)
+        ws, ws_bytes, _alive = c.workspace(workspace, need)
+        dw_type = _type(dw.dtype) if need_dw else shape.type
+        head = (ctypes.byref(shape), py, ldy)
+        tail = (px, ldx, pw, po, pdx, lddx, pdw, dw_type, ws, ws_bytes, c.stream)
+        if gated:
+            pg, ldg = c.rows("gate_up", gate_up, rows, 2 * n, dtype)
+            _lib.check(c.lib.moe_gated_product_backward(*head, pg, ldg, *tail))
+        else:
+            _lib.check(c.lib.moe_expert_product_backward(*head, *tail))
+    return dx, dw
+
+
+def expert_product_backward(dy, x, w, offsets=None, need_dx=True, need_dw=True, dx=None, dw=None, dw_dtype=None,
+                            workspace=None, stream=None):
+    """(dx, dw) of expert_product for the gradient dy [rows, n]: dx = dy w[e], dw[e] = dy_e^T x_e (of w's
+    dtype, or `dw_dtype` fp32; zero for a group without rows).  What is not needed is None."""
+    return _backward("expert_product_backward", dy, None, x, w, offsets, None, need_dx, need_dw, dx, dw, dw_dtype,
+                     workspace, stream)
+
+
+def gated_product_backward(dh, gate_up, x, w, offsets=None, activation="silu", need_dx=True, need_dw=True, dx=None,
+                           dw=None, dw_dtype=None, workspace=None, stream=None):
+    """(dx, dw) of gated_product for the gradient dh [rows, n] and the gate_up it saved."""
+    return _backward("gated_product_backward", dh, gate_up, x, w, offsets, activation or "silu", need_dx, need_dw, dx,
+                     dw, dw_dtype, workspace, stream)

@@ -1,0 +1,196 @@
+"""Host-only tests of the grouped products' C ABI: shapes and arguments are
+refused before anything is enqueued.  Nothing here launches a kernel."""
+
+import ctypes
+import os
+
+import pytest
+
+from expert_ffn_layer_router_amd import _lib
+
+FAKE = 0x10000  # an aligned address that validation never dereferences
+BF16, FP16, FP32 = _lib.MOE_TYPE_BF16, _lib.MOE_TYPE_FP16, _lib.MOE_TYPE_FP32
+INVALID, SHAPE, SMALL = _lib.MOE_ERR_INVALID_ARG, _lib.MOE_ERR_UNSUPPORTED_SHAPE, _lib.MOE_ERR_WORKSPACE_TOO_SMALL
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_lib.LIB_PATH):
+        from expert_ffn_layer_router_amd import build
+        build.build()
+    return _lib.load()
+
+
+def shape(**kw):
+    base = dict(rows=0, n=64, k=64, groups=1, type=BF16, activation=0)
+    base.update(kw)
+    return _lib.MoeProduct(**base)
+
+
+def workspace(lib, op, **kw):
+    n = ctypes.c_size_t()
+    st = lib.moe_product_workspace(ctypes.byref(shape(**kw)), _lib.MOE_OPS[op], ctypes.byref(n))
+    return st, n.value
+
+
+@pytest.mark.parametrize("op", sorted(_lib.MOE_OPS))
+@pytest.mark.parametrize("kw", [dict(rows=-1), dict(rows=(1 << 22) + 1), dict(n=0), dict(n=12), dict(n=65544),
+                                dict(k=0), dict(k=12), dict(k=65552), dict(groups=0), dict(groups=257),
+                                dict(type=3), dict(type=-1), dict(activation=2), dict(activation=-1)])
+def test_shapes_refused(lib, op, kw):
+    assert workspace(lib, op, **kw)[0] == SHAPE, _lib.last_error()
+
+
+def test_shapes_by_operator(lib):
+    assert workspace(lib, "expert_product", k=24)[0] == 0
+    assert workspace(lib, "int8_product", k=24)[0] == SHAPE  # codes come in 16s
+    assert workspace(lib, "int8_product", type=FP32)[0] == 0
+    for op in ("int8_gated", "expert_product", "gated_product", "expert_product_backward", "gated_product_backward"):
+        assert workspace(lib, op, type=FP32)[0] == SHAPE
+    for op in ("int8_gated", "gated_product", "gated_product_backward"):
+        assert workspace(lib, op, n=32768)[0] == 0
+        assert workspace(lib, op, n=32776)[0] == SHAPE
+        assert workspace(lib, op, activation=1)[0] == 0
+    for op in ("int8_product", "expert_product", "expert_product_backward"):
+        assert workspace(lib, op, activation=1)[0] == SHAPE
+    n = ctypes.c_size_t()
+    assert lib.moe_product_workspace(None, 0, ctypes.byref(n)) == INVALID
+    assert lib.moe_product_workspace(ctypes.byref(shape()), 6, ctypes.byref(n)) == INVALID
+    assert lib.moe_product_workspace(ctypes.byref(shape()), -1, ctypes.byref(n)) == INVALID
+    assert lib.moe_product_workspace(ctypes.byref(shape()), 0, None) == INVALID
+
+
+def test_workspace_holds_the_slopes_and_the_parts(lib):
+    # (dg, du) of the gated backward pass
+    st, n = workspace(lib, "gated_product_backward", rows=1000, n=4096, k=4096)
+    assert st == 0 and n >= 1000 * 2 * 4096 * 2
+    # a few rows past the streaming kernel and a narrow result: the contraction is split
+    st, n = workspace(lib, "expert_product", rows=100, n=128, k=8192)
+    assert st == 0 and n > 0 and n % (100 * 128 * 4) < 256
+    # many blocks: no split
+    assert workspace(lib, "expert_product", rows=4096, n=8192, k=4096) == (0, 0)
+    assert workspace(lib, "expert_product", rows=0, n=128, k=8192) == (0, 0)
+    # the largest shapes stay in range of the size type
+    st, n = workspace(lib, "gated_product_backward", rows=1 << 22, n=32768, k=65536, groups=256)
+    assert st == 0 and n >= (1 << 22) * 65536 * 2
+
+
+def forward(lib, op, **over):
+    """A call that fails validation or has no rows (never launches)."""
+    fields = {f: over.pop(f) for f in list(over) if f in dict(_lib.MoeProduct._fields_)}
+    p = shape(**fields)
+    a = dict(x=FAKE, ldx=p.k, scale=FAKE, w=FAKE, w_scale=FAKE, offsets=None, out=FAKE, ldout=p.n, gate_up=None,
+             ldgu=2 * p.n, ws=FAKE, ws_bytes=1 << 40)
+    a.update(over)
+    ref = ctypes.byref(p)
+    end = (a["ws"], a["ws_bytes"], None)
+    if op.startswith("int8"):
+        return getattr(lib, "moe_" + op)(ref, a["x"], a["ldx"], a["scale"], a["w"], a["w_scale"], a["offsets"],
+                                         a["out"], a["ldout"], *end)
+    if op == "expert_product":
+        return lib.moe_expert_product(ref, a["x"], a["ldx"], a["w"], a["offsets"], a["out"], a["ldout"], *end)
+    return lib.moe_gated_product(ref, a["x"], a["ldx"], a["w"], a["offsets"], a["out"], a["ldout"], a["gate_up"],
+                                 a["ldgu"], *end)
+
+
+@pytest.mark.parametrize("op", ["int8_product", "int8_gated", "expert_product", "gated_product"])
+def test_forward_arguments_refused(lib, op):
+    assert forward(lib, op) == 0  # no rows: nothing to do
+    assert forward(lib, op, x=None, scale=None, out=None) == 0
+    assert forward(lib, op, rows=4, x=None) == INVALID
+    assert forward(lib, op, rows=4, x=FAKE + 8) == INVALID
+    assert forward(lib, op, rows=4, ldx=48) == INVALID           # shorter than a row
+    assert forward(lib, op, rows=4, ldx=68) == INVALID           # rows off their alignment
+    assert forward(lib, op, rows=4, ldx=(1 << 20) + 16) == INVALID
+    assert forward(lib, op, rows=4, w=None) == INVALID
+    assert forward(lib, op, rows=4, w=FAKE + 2) == INVALID
+    assert forward(lib, op, rows=4, out=None) == INVALID
+    assert forward(lib, op, rows=4, out=FAKE + 4) == INVALID
+    assert forward(lib, op, rows=4, ldout=56) == INVALID
+    assert forward(lib, op, rows=4, ldout=66) == INVALID
+    assert forward(lib, op, rows=4, groups=2) == INVALID         # groups without offsets
+    assert forward(lib, op, rows=4, groups=2, offsets=FAKE + 2) == INVALID
+    assert forward(lib, op, rows=100, n=128, k=8192, ws_bytes=1) == SMALL
+    assert "needs" in _lib.last_error()
+    assert forward(lib, op, rows=100, n=128, k=8192, ws=None, ws_bytes=1 << 40) == INVALID
+    assert forward(lib, op, rows=100, n=128, k=8192, ws=FAKE + 8) == INVALID
+    if op.startswith("int8"):
+        assert forward(lib, op, rows=4, scale=None) == INVALID
+        assert forward(lib, op, rows=4, w_scale=None) == INVALID
+        assert forward(lib, op, rows=4, ldx=72) == INVALID       # codes come in 16s
+    if op == "gated_product":
+        assert forward(lib, op, rows=4, gate_up=FAKE, ldgu=64) == INVALID
+        assert forward(lib, op, rows=4, gate_up=FAKE + 8) == INVALID
+
+
+def backward(lib, gated, **over):
+    fields = {f: over.pop(f) for f in list(over) if f in dict(_lib.MoeProduct._fields_)}
+    p = shape(**fields)
+    a = dict(dy=FAKE, lddy=p.n, gu=FAKE, ldgu=2 * p.n, x=FAKE, ldx=p.k, w=FAKE, offsets=None, dx=FAKE, lddx=p.k,
+             dw=None, dw_type=p.type, ws=FAKE, ws_bytes=1 << 40)
+    a.update(over)
+    head = (ctypes.byref(p), a["dy"], a["lddy"])
+    tail = (a["x"], a["ldx"], a["w"], a["offsets"], a["dx"], a["lddx"], a["dw"], a["dw_type"], a["ws"], a["ws_bytes"],
+            None)
+    if gated:
+        return lib.moe_gated_product_backward(*head, a["gu"], a["ldgu"], *tail)
+    return lib.moe_expert_product_backward(*head, *tail)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_backward_arguments_refused(lib, gated):
+    assert backward(lib, gated) == 0                              # no rows and no dw: nothing to do
+    assert backward(lib, gated, rows=4, dx=None, dw=None) == 0    # nothing asked for
+    assert backward(lib, gated, rows=4, dy=None) == INVALID
+    assert backward(lib, gated, rows=4, lddy=60) == INVALID
+    assert backward(lib, gated, rows=4, dx=FAKE + 8) == INVALID
+    assert backward(lib, gated, rows=4, lddx=56) == INVALID
+    assert backward(lib, gated, rows=4, w=None) == INVALID
+    assert backward(lib, gated, rows=4, dw=FAKE + 8) == INVALID
+    assert backward(lib, gated, rows=4, dw=FAKE, x=None) == INVALID
+    assert backward(lib, gated, rows=4, dw=FAKE, ldx=60) == INVALID
+    assert backward(lib, gated, rows=4, dw=FAKE, dw_type=FP16) == SHAPE   # bf16 operands
+    assert backward(lib, gated, rows=4, groups=3) == INVALID
+    # the sums over 8192 values of n are split
+    assert backward(lib, gated, rows=100, n=8192, k=128, ws_bytes=0) == SMALL
+    if gated:
+        assert backward(lib, gated, rows=4, gu=None) == INVALID
+        assert backward(lib, gated, rows=4, ldgu=64) == INVALID
+        assert backward(lib, gated, rows=4, ws=None) == INVALID
+
+
+def test_quantize_arguments_refused(lib):
+    def call(rows=4, k=64, type_=BF16, x=FAKE, ldx=64, codes=FAKE, ldc=64, scale=FAKE):
+        return lib.moe_quantize_rows(rows, k, type_, x, ldx, codes, ldc, scale, None)
+
+    assert call(rows=0) == 0
+    assert call(rows=0, x=None, codes=None, scale=None) == 0
+    for kw in (dict(rows=-1), dict(rows=(1 << 22) + 1), dict(k=0), dict(k=8), dict(k=24), dict(k=65552),
+               dict(type_=FP32), dict(type_=-1)):
+        assert call(**kw) == SHAPE, kw
+    for kw in (dict(x=None), dict(x=FAKE + 2), dict(ldx=56), dict(ldx=68), dict(codes=None), dict(codes=FAKE + 8),
+               dict(ldc=48), dict(ldc=72), dict(scale=None), dict(scale=FAKE + 2)):
+        assert call(**kw) == INVALID, kw
+
+
+def test_binding_refuses_what_the_library_cannot_see():
+    import torch
+
+    import expert_ffn_layer_router_amd as moe
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    w = torch.zeros(1, 64, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        moe.expert_product(x, w)
+    with pytest.raises(ValueError, match="matrix"):
+        moe.expert_product(x[0], w)
+    with pytest.raises(ValueError, match="w must be"):
+        moe.expert_product(x, w[0, 0])
+    with pytest.raises(ValueError, match="equal numbers"):
+        moe.gated_product(x, torch.zeros(7, 64, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="op must be"):
+        moe.product_workspace("product", 1, 8, 8)
+    with pytest.raises(ValueError, match="activation"):
+        moe.product_workspace("gated_product", 1, 8, 8, activation="tanh")
+    with pytest.raises(moe.MoeError) as e:
+        moe.product_workspace("expert_product", 1, 12, 8)
+    assert e.value.status == SHAPE
