@@ -37,20 +37,26 @@ ProductPlan plan_product(Num num, Pass pass, Result res, const ProductArgs& a) {
     const int64_t m = (int64_t)a.groups * ceil_div(wg ? a.wrows : group_rows, tile);
     return m * ceil_div(cols, gated ? tile / 2 : tile);
   };
-  if (blocks(256) >= 256 && (wg || group_rows > 128)) {
-    p.family = Family::kTile256;
-    return p;
-  }
-  p.family = Family::kTile128;
-  // fewer than one block per compute unit: split the contraction, in parts
-  // of at least 4 stages
-  const int64_t n = blocks(128);
+  const bool large = blocks(256) >= 256 && (wg || group_rows > 128);
+  p.family = large ? Family::kTile256 : Family::kTile128;
+  const int tile = large ? 256 : 128;
   const int stages = ceil_div(wg ? group_rows : a.contract, num == Num::kInt8 ? 128 : 64);
-  if (n < 256) p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({8, 512 / n, stages / 4}));
-  if (p.splits > 1) {
-    const size_t rows = wg ? (size_t)a.groups * a.wrows : (size_t)a.rows;
-    p.partial_bytes = align_up((size_t)p.splits * rows * a.cols * 4);
+  size_t units;
+  if (wg) {
+    // fewer tiles than the compute units hold: split the contraction, in
+    // parts of at least 4 stages of an average group
+    const int64_t tiles = blocks(tile);
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({8, 512 / tiles, stages / 4}));
+    if (large) p.splits = 1;
+    units = tiles * p.splits;
+  } else {
+    // the most parts of a tile that can pay (rounds_of)
+    const int64_t tiles = (int64_t)row_tile_bound(a.rows, a.groups, tile) * ceil_div(cols, gated ? tile / 2 : tile);
+    p.splits = std::max(1, std::min(8, stages / 4));
+    if (stages * (p.splits - 1) / p.splits <= 6) p.splits = 1;
+    units = split_units(tile, (int)std::min<int64_t>(tiles, 1 << 20), p.splits);
   }
+  if (p.splits > 1) p.partial_bytes = units * tile * tile * 4;
   return p;
 }
 
@@ -195,7 +201,6 @@ void enqueue(ProductArgs& a, const ProductPlan& plan, Num num, Pass pass, Result
     launch_product_half(a, plan, num, res, s);
   else
     launch_product_grad(a, plan, num, pass, res, s);
-  if (plan.splits > 1) launch_product_join(a, num, pass, res, s);
 }
 
 moe_status forward(const moe_product* p, moe_op op, const void* x, int64_t ldx, const float* scale, const void* w,

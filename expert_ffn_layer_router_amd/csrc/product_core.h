@@ -3,6 +3,8 @@
 // matrix-core kernel.
 #pragma once
 
+#include <algorithm>
+
 #include "device_common.h"
 #include "products.h"
 
@@ -134,21 +136,51 @@ __device__ __forceinline__ int xcd_unit(int b, int units) {
   return i < q + (x < r) ? x * q + min(x, r) + i : -1;
 }
 
+// One unit of a tiled product: a tile, or one part of a tile's contraction.
 struct RowTile {
   int group, row0, end, tile_n;  // group; first row; end of the group's rows; column tile
+  int part, parts;               // this unit's share of the contraction
+  int slot, slot_step;           // parts > 1: where its raw sums go, and from one part to the next
 };
+
+// How the tiles of a forward product or an input gradient go to the compute
+// units, which hold `slots` blocks at a time: the tiles beyond the last full
+// round would occupy rem = tiles mod slots of them for a whole tile's time, so
+// their contraction is split in up to slots / rem parts.  Worth it where the
+// saved stages outweigh the raw sums' way through memory and the joining
+// kernel; a part keeps at least 4 stages.
+struct Rounds {
+  int full, rem, parts;
+};
+template <int BM, int BN>
+__host__ __device__ __forceinline__ Rounds rounds_of(int tiles, int stages, int max_parts) {
+  constexpr int slots = BM == 256 ? 256 : 512;
+  Rounds r;
+  r.full = tiles / slots * slots;
+  r.rem = tiles - r.full;
+  r.parts = 1;
+  if (r.rem) {
+    int s = slots / r.rem;
+    s = s < max_parts ? s : max_parts;
+    s = s < stages / 4 ? s : stages / 4;
+    const int cost = BM == 256 ? 6 + r.rem * s / 8 : 6 + r.rem * s / 32;  // in stages
+    if (s > 1 && stages * (s - 1) / s > cost) r.parts = s;
+  }
+  return r;
+}
 
 // This block's row tile (BM rows of one group) and column tile: tiles are
 // counted over the groups (at most 256, one thread each), dealt by xcd_unit,
 // and walked in bands of kBand row tiles so that blocks running side by side
-// share weight columns and rows.  `scratch`: 1100 bytes of LDS, free again
-// after the caller's next barrier.  Every thread calls it.
+// share weight columns and rows.  JOIN: block b has the b-th split tile.
+// `scratch`: 28 bytes of LDS, free again after the caller's next barrier.
+// Every thread calls it.
 constexpr int kBand = 8;
-template <int BM, int THREADS>
-__device__ __forceinline__ bool find_row_tile(const ProductArgs& a, int tiles_n, lds_char* scratch, RowTile& t) {
-  __attribute__((address_space(3))) int* incl = (__attribute__((address_space(3))) int*)scratch;  // [256] inclusive tile counts
-  __attribute__((address_space(3))) int* wsum = incl + 256;                                        // [4]
-  __attribute__((address_space(3))) int* found = incl + 260;                                       // [3]
+template <int BM, int BN, int THREADS, bool JOIN>
+__device__ __forceinline__ bool find_row_tile(const ProductArgs& a, int tiles_n, int stages, lds_char* scratch, RowTile& t) {
+  typedef __attribute__((address_space(3))) int lds_int;
+  lds_int* wsum = (lds_int*)scratch;  // [4] tiles of 64 groups each
+  lds_int* found = wsum + 4;          // [3]
   const int tid = threadIdx.x;
   int tiles_m;
   int begin = 0, end = a.rows, mine = 0, upto = 0;
@@ -176,18 +208,45 @@ __device__ __forceinline__ bool find_row_tile(const ProductArgs& a, int tiles_n,
       tiles_m += wsum[w];
     }
   }
-  // the grid is sized for offsets in order: with others some rows stay unspecified
-  tiles_m = __builtin_amdgcn_readfirstlane(tiles_m);
-  const int unit = xcd_unit(blockIdx.x, tiles_m * tiles_n);
+  // the grid and the raw sums' space are sized for offsets in order, which
+  // have at most this many tiles: with others some rows stay unspecified
+  tiles_m = __builtin_amdgcn_readfirstlane(min(tiles_m, row_tile_bound(a.rows, a.groups, BM)));
+  const Rounds r = rounds_of<BM, BN>(tiles_m * tiles_n, stages, a.splits);
+  const int whole = r.full + (r.parts == 1 ? r.rem : 0);
+  int unit;
+  t.part = 0;
+  t.parts = 1;
+  t.slot = t.slot_step = 0;
+  const int b = blockIdx.x, padded = (whole + 7) / 8 * 8;
+  if (JOIN) {
+    if (r.parts == 1 || b >= r.rem) return false;
+    unit = whole + b;
+  } else if (b < padded) {
+    unit = xcd_unit(b, whole);
+  } else {
+    if (r.parts == 1) return false;
+    const int u = xcd_unit(b - padded, r.rem * r.parts);
+    if (u < 0) return false;
+    // neighbours take the same part of neighbouring tiles: they share operands
+    t.part = u / r.rem;
+    unit = whole + u % r.rem;
+  }
   if (unit < 0) return false;
+  if (unit >= whole) {
+    t.parts = r.parts;
+    t.slot = t.part * r.rem + (unit - whole);
+    t.slot_step = r.rem;
+  }
   const int band = unit / (kBand * tiles_n), in = unit % (kBand * tiles_n);
   const int high = min(kBand, tiles_m - band * kBand);
   const int m = band * kBand + in % high;
   t.tile_n = in / high;
   if (a.groups == 1) {
+    // uniform, but the compiler cannot see it: the copies' descriptors must
+    // stay in scalar registers
     t.group = 0;
-    t.row0 = begin + m * BM;
-    t.end = end;
+    t.row0 = __builtin_amdgcn_readfirstlane(begin + m * BM);
+    t.end = __builtin_amdgcn_readfirstlane(end);
     return true;
   }
   if (tid < 256 && m < upto && m >= upto - mine) {
@@ -227,7 +286,10 @@ __device__ __forceinline__ bool find_row_tile(const ProductArgs& a, int tiles_n,
 //
 // Gated: the block's columns are BN/2 gate and the same BN/2 up columns,
 // interleaved by 32 so that a wave holds g and u of the same elements.
-template <Num T, Pass PASS, Result RES, bool SPLIT, int BM, int BN, int WM, int WN>
+//
+// JOIN: the block adds the raw sums of a split tile's parts, in order, instead
+// of computing them, and writes the result.
+template <Num T, Pass PASS, Result RES, bool JOIN, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductArgs a) {
   constexpr int NW = WM * WN, THREADS = 64 * NW;
   constexpr int MI = BM / 32 / WM, NJ = BN / 32 / WN;
@@ -254,43 +316,70 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   const int tiles_n = (ncols + NO - 1) / NO;
 
   // this block's rows [row0, row0 + live) and columns [n0, ...), its group,
-  // and the contraction's length
-  int group, row0, live, n0, klen;
+  // the contraction's length and this block's stages of it
+  int group, row0, live, n0, klen, part, parts, slot, slot_step;
+  int gbegin = 0;
   if constexpr (PASS == Pass::kWeightGrad) {
-    const int tiles_m = (a.wrows + BM - 1) / BM;
-    const int unit = xcd_unit(blockIdx.x, a.groups * tiles_m * tiles_n);
-    if (unit < 0) return;
-    group = unit / (tiles_m * tiles_n);
-    const int in = unit % (tiles_m * tiles_n);
+    // every group's tiles are spread over all XCDs: the groups' contractions
+    // differ in length
+    const int tiles_m = (a.wrows + BM - 1) / BM, tiles = tiles_m * tiles_n, padded = (tiles + 7) / 8 * 8;
+    const int b = blockIdx.x;
+    const int in = JOIN ? b % tiles : xcd_unit(b % padded, tiles);
+    if (in < 0) return;
+    group = (JOIN ? b / tiles : b / padded) % a.groups;
+    parts = a.splits;
+    part = JOIN ? 0 : b / (padded * a.groups);
+    slot = (part * a.groups + group) * tiles + in;
+    slot_step = a.groups * tiles;
     const int band = in / (kBand * tiles_n), high = min(kBand, tiles_m - band * kBand);
     row0 = (band * kBand + in % (kBand * tiles_n) % high) * BM;
     n0 = in % (kBand * tiles_n) / high * NO;
     live = min(BM, a.wrows - row0);
-  } else {
-    RowTile t;
-    if (!find_row_tile<BM, THREADS>(a, tiles_n, smem, t)) return;
-    group = t.group;
-    row0 = t.row0;
-    live = min(BM, t.end - t.row0);
-    n0 = t.tile_n * NO;
-    if (a.groups > 1) __syncthreads();  // the lookup's LDS is free
-  }
-  int gbegin = 0;
-  if constexpr (PASS == Pass::kWeightGrad) {
     int gend;
     group_rows(a.offsets, a.rows, group, gbegin, gend);
     klen = __builtin_amdgcn_readfirstlane(gend - gbegin);
     gbegin = __builtin_amdgcn_readfirstlane(gbegin);
   } else {
     klen = a.contract;
+    RowTile t;
+    if (!find_row_tile<BM, BN, THREADS, JOIN>(a, tiles_n, (klen + BK - 1) / BK, smem, t)) return;
+    group = t.group;
+    row0 = t.row0;
+    live = min(BM, t.end - t.row0);
+    n0 = t.tile_n * NO;
+    part = t.part;
+    parts = t.parts;
+    slot = t.slot;
+    slot_step = t.slot_step;
+    if (a.groups > 1) __syncthreads();  // the lookup's LDS is free
   }
-  int st0 = 0, st1 = (klen + BK - 1) / BK;
-  if constexpr (SPLIT) {
-    const int all = st1;
-    st0 = (int)((int64_t)all * blockIdx.z / a.splits);
-    st1 = (int)((int64_t)all * (blockIdx.z + 1) / a.splits);
-  }
+  const int stages = (klen + BK - 1) / BK;
+  const int st0 = (int)((int64_t)stages * part / parts), st1 = (int)((int64_t)stages * (part + 1) / parts);
+  // raw sums of a part: every lane's, 16 bytes each
+  auto raw = [&](int at, int i, int j, int q) {
+    using t4 = typename Acc<T>::t4;
+    return reinterpret_cast<t4*>(a.partial + (int64_t)at * (BM * BN * 4)) +
+           (((wave * MI + i) * NJ + j) * 4 + q) * 64 + lane;
+  };
 
+  acc_t acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = acc_t{};
+  if constexpr (JOIN) {
+    for (int s = 0; s < parts; ++s)
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const typename Acc<T>::t4 v = *raw(slot + s * slot_step, i, j, q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
+          }
+  } else {
   // ---- copies ----
   const char* pbase = P_STR ? a.p + (int64_t)gbegin * a.ldp + (int64_t)row0 * ES : a.p + (int64_t)row0 * a.ldp;
   const char* qbase;
@@ -382,11 +471,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
     for (int i = 0; i < MI; ++i) pf[i] = fragment(P_STR, BM, b + pat[i], s);
   };
 
-  acc_t acc[MI][NJ];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[i][j] = acc_t{};
   auto products = [&](u32x4(&pf)[MI], u32x4(&qf)[NJ]) {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -429,33 +513,25 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
     }
   }
 
+  if (parts > 1) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *raw(slot, i, j, q) = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    return;
+  }
+  }  // !JOIN
+
   // ---- results ----
   // element e of acc[i][j]: row rowl(i), column coll(j) + 8 (e / 4) + e % 4
   auto rowl = [&](int i) { return (wm * MI + i) * 32 + l32; };
   auto coll = [&](int j) {
     return (GATED ? (wn * (NJ / 2) + j / 2) * 32 : (wn * NJ + j) * 32) + 4 * hh;
   };
-  if constexpr (SPLIT) {
-    // raw sums: column c of the product (gated: the up columns from F on)
-    const int64_t all_rows = PASS == Pass::kWeightGrad ? (int64_t)a.groups * a.wrows : a.rows;
-    const int64_t base_row = PASS == Pass::kWeightGrad ? (int64_t)group * a.wrows + row0 : row0;
-    using t4 = typename Acc<T>::t4;
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      if (rowl(i) >= live) continue;
-      char* rowp = a.partial + ((int64_t)blockIdx.z * all_rows + base_row + rowl(i)) * a.cols * 4;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c = n0 + coll(j) + 8 * q;
-          if (c < ncols)
-            *reinterpret_cast<t4*>(rowp + (int64_t)(c + (GATED && j % 2 ? F : 0)) * 4) =
-                t4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        }
-    }
-    return;
-  } else {
+  {
     const bool fp16 = T == Num::kFp16 || (T == Num::kInt8 && a.out_type == MOE_TYPE_FP16);
     // codes: the sum times the row's and the column's scale
     float prow[MI];
@@ -548,34 +624,33 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   }
 }
 
-// Row tiles a grid must hold: sum_e ceil(rows_e / BM) is at most this.
-inline int row_tile_bound(int rows, int groups, int bm) {
-  return (rows + bm - 1) / bm + (rows < groups ? rows : groups) - (groups > 0 && rows > 0 ? 1 : 0);
-}
-
-template <Num T, Pass PASS, Result RES, bool SPLIT, int BM, int BN, int WM, int WN>
+template <Num T, Pass PASS, Result RES, int BM, int BN, int WM, int WN>
 void launch_tile(const ProductArgs& a, hipStream_t s) {
   const int no = RES == Result::kGated ? BN / 2 : BN;
-  const int ncols = RES == Result::kGated ? a.cols / 2 : a.cols;
-  const int tiles_n = (ncols + no - 1) / no;
-  const int tiles_m = PASS == Pass::kWeightGrad ? a.groups * ((a.wrows + BM - 1) / BM)
-                                                : row_tile_bound(a.rows, a.offsets ? a.groups : 1, BM);
-  // xcd_unit deals units in rounds of 8
-  const int blocks = (tiles_m * tiles_n + 7) / 8 * 8;
-  product_tile_kernel<T, PASS, RES, SPLIT, BM, BN, WM, WN>
-      <<<dim3(blocks, 1, SPLIT ? a.splits : 1), 64 * WM * WN, 0, s>>>(a);
+  const int tiles_n = ((RES == Result::kGated ? a.cols / 2 : a.cols) + no - 1) / no;
+  const int threads = 64 * WM * WN;
+  int blocks, joins;
+  if (PASS == Pass::kWeightGrad) {
+    const int tiles = (a.wrows + BM - 1) / BM * tiles_n;
+    blocks = a.splits * a.groups * ((tiles + 7) / 8 * 8);  // xcd_unit deals units in rounds of 8
+    joins = a.groups * tiles;
+  } else {
+    const int tiles = row_tile_bound(a.rows, a.groups, BM) * tiles_n;
+    blocks = (tiles + 7) / 8 * 8 + (a.splits > 1 ? split_units(BM, tiles, a.splits) + 8 : 0);
+    joins = std::min(tiles, (BM == 256 ? 256 : 512) / 2);  // a split tile has at least two parts
+  }
+  product_tile_kernel<T, PASS, RES, false, BM, BN, WM, WN><<<blocks, threads, 0, s>>>(a);
+  if (a.splits > 1) product_tile_kernel<T, PASS, RES, true, BM, BN, WM, WN><<<joins, threads, 0, s>>>(a);
 }
 
 // The 128 x 128 (4 waves, two blocks per compute unit) or 256 x 256 (8 waves)
-// block, whole or with the contraction split.
+// block.
 template <Num T, Pass PASS, Result RES>
 void launch_tiles(const ProductArgs& a, const ProductPlan& p, hipStream_t s) {
   if (p.family == Family::kTile256)
-    launch_tile<T, PASS, RES, false, 256, 256, 2, 4>(a, s);
-  else if (p.splits == 1)
-    launch_tile<T, PASS, RES, false, 128, 128, 2, 2>(a, s);
+    launch_tile<T, PASS, RES, 256, 256, 2, 4>(a, s);
   else
-    launch_tile<T, PASS, RES == Result::kWide ? Result::kHalf : RES, true, 128, 128, 2, 2>(a, s);
+    launch_tile<T, PASS, RES, 128, 128, 2, 2>(a, s);
 }
 
 }  // namespace moe

@@ -1,5 +1,5 @@
-// The element-wise parts of the grouped products: quantising rows, joining
-// the parts of a split contraction, and the gated block's slopes.
+// The element-wise parts of the grouped products: quantising rows and the
+// gated block's slopes.
 #include <type_traits>
 
 #include "product_core.h"
@@ -95,70 +95,6 @@ __global__ __launch_bounds__(256) void quantize_kernel(int rows, int k, bool fp1
   for (int i = t + CH * kThreads; i < chunks; i += kThreads) store(i, src[i]);
 }
 
-// ---- join of a split contraction ------------------------------------------------
-// out = result of the sum of `splits` raw parts, four columns per thread, the
-// parts added in order.
-template <Num T, Result RES, bool WEIGHT_GRAD>
-__global__ __launch_bounds__(256) void join_kernel(ProductArgs a) {
-  constexpr bool GATED = RES == Result::kGated;
-  using t4 = typename Acc<T>::t4;
-  const int F = a.cols / 2, quads = (GATED ? F : a.cols) / 4;
-  const int64_t all = WEIGHT_GRAD ? (int64_t)a.groups * a.wrows : a.rows;
-  const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t row = at / quads;
-  const int col = (int)(at % quads) * 4;
-  if (row >= all) return;
-  if constexpr (!WEIGHT_GRAD) {
-    // rows outside every group have no parts
-    int begin, end;
-    group_rows(a.offsets, a.rows, 0, begin, end);
-    if (a.offsets) end = max(0, min(a.offsets[a.groups], a.rows));
-    if (row < begin || row >= end) return;
-  }
-  int group = 0;
-  if (T == Num::kInt8 && a.offsets) {
-    // the last group that begins at or before the row: its own (ascending offsets)
-    int lo = 0, hi = a.groups;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (a.offsets[mid] <= row) lo = mid; else hi = mid;
-    }
-    group = lo;
-  }
-  auto total = [&](int c) -> f32x4 {
-    const char* src = a.partial + (row * a.cols + c) * 4;
-    t4 v = *reinterpret_cast<const t4*>(src);
-    for (int s = 1; s < a.splits; ++s) v += *reinterpret_cast<const t4*>(src + (int64_t)s * all * a.cols * 4);
-    f32x4 f;
-    if constexpr (T == Num::kInt8) {
-      const float ps = a.pscale[row];
-      const f32x4 qs = *reinterpret_cast<const f32x4*>(a.qscale + (int64_t)group * a.cols + c);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] = (float)v[e] * ps * qs[e];
-    } else {
-      f = v;
-    }
-    return f;
-  };
-  f32x4 v = total(col);
-  const bool fp16 = T == Num::kFp16 || (T == Num::kInt8 && a.out_type == MOE_TYPE_FP16);
-  if constexpr (GATED) {
-    const f32x4 u = total(F + col);
-    if (T != Num::kInt8 && a.keep) {
-      uint16_t* k = a.keep + row * a.ldkeep + col;
-      *reinterpret_cast<u32x2*>(k) = u32x2{pack_half(fp16, v[0], v[1]), pack_half(fp16, v[2], v[3])};
-      *reinterpret_cast<u32x2*>(k + F) = u32x2{pack_half(fp16, u[0], u[1]), pack_half(fp16, u[2], u[3])};
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = activate(a.act, v[e]) * u[e];
-  }
-  if constexpr (RES == Result::kWide)
-    *reinterpret_cast<f32x4*>((float*)a.out + row * a.ldout + col) = v;
-  else
-    *reinterpret_cast<u32x2*>((uint16_t*)a.out + row * a.ldout + col) =
-        u32x2{pack_half(fp16, v[0], v[1]), pack_half(fp16, v[2], v[3])};
-}
-
 // ---- slopes of the gated block ------------------------------------------------
 // dg = dh u act'(g), du = dh act(g); 8 columns per thread.  Bound by memory:
 // 10 bytes per element of dh.
@@ -195,44 +131,7 @@ __global__ __launch_bounds__(256) void gated_slopes_kernel(int rows, int n, bool
   *reinterpret_cast<u32x4*>(dgu + row * 2 * n + n + col) = ou;
 }
 
-template <Num T, Result RES, bool WG>
-void launch_join(const ProductArgs& a, hipStream_t s) {
-  const int64_t rows = WG ? (int64_t)a.groups * a.wrows : a.rows;
-  const int64_t quads = rows * ((RES == Result::kGated ? a.cols / 2 : a.cols) / 4);
-  join_kernel<T, RES, WG><<<(unsigned)((quads + 255) / 256), 256, 0, s>>>(a);
-}
-
 }  // namespace
-
-void launch_product_join(const ProductArgs& a, Num num, Pass pass, Result res, hipStream_t s) {
-  if (num == Num::kInt8) {
-    if (res == Result::kGated)
-      launch_join<Num::kInt8, Result::kGated, false>(a, s);
-    else if (res == Result::kWide)
-      launch_join<Num::kInt8, Result::kWide, false>(a, s);
-    else
-      launch_join<Num::kInt8, Result::kHalf, false>(a, s);
-    return;
-  }
-  const bool wg = pass == Pass::kWeightGrad;
-  if (res == Result::kWide) {
-    launch_join<Num::kBf16, Result::kWide, true>(a, s);  // fp32 sums to fp32: the operands' type is gone
-  } else if (num == Num::kFp16) {
-    if (res == Result::kGated)
-      launch_join<Num::kFp16, Result::kGated, false>(a, s);
-    else if (wg)
-      launch_join<Num::kFp16, Result::kHalf, true>(a, s);
-    else
-      launch_join<Num::kFp16, Result::kHalf, false>(a, s);
-  } else {
-    if (res == Result::kGated)
-      launch_join<Num::kBf16, Result::kGated, false>(a, s);
-    else if (wg)
-      launch_join<Num::kBf16, Result::kHalf, true>(a, s);
-    else
-      launch_join<Num::kBf16, Result::kHalf, false>(a, s);
-  }
-}
 
 void launch_quantize(int rows, int k, int type, const uint16_t* x, int64_t ldx, int8_t* codes, int64_t ldcodes,
                      float* scale, hipStream_t s) {

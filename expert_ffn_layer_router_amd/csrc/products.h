@@ -34,8 +34,9 @@ struct ProductArgs {
   const float* pscale = nullptr;   // codes: scale of each row, of each w row ([groups][cols])
   const float* qscale = nullptr;
   int act = 0;
-  // contraction split: this many parts, their raw sums in `partial`
-  // [splits][rows or groups * wrows][cols], joined by a second kernel
+  // contraction split: weight gradient, into this many parts; otherwise the
+  // most parts that the kernels may choose (rounds_of), 1 if none can pay.
+  // The parts' raw sums go to `partial`; a second launch joins them.
   int splits = 1;
   char* partial = nullptr;
 };
@@ -48,6 +49,16 @@ struct ProductPlan {
   size_t partial_bytes = 0;
 };
 
+// Row tiles a grid must hold: sum_e ceil(rows_e / bm) is at most this.
+__host__ __device__ inline int row_tile_bound(int rows, int groups, int bm) {
+  return (rows + bm - 1) / bm + (rows < groups ? rows : groups) - (rows > 0 ? 1 : 0);
+}
+// Parts of split tiles that a product of at most `tiles` tiles can have.
+inline int split_units(int bm, int tiles, int max_parts) {
+  const int slots = bm == 256 ? 256 : 512;
+  return (int64_t)tiles * max_parts < slots ? tiles * max_parts : slots;
+}
+
 // Pure host arithmetic.
 ProductPlan plan_product(Num num, Pass pass, Result res, const ProductArgs& a);
 
@@ -56,7 +67,6 @@ void launch_product_int8(const ProductArgs& a, const ProductPlan& p, Result res,
 void launch_product_half(const ProductArgs& a, const ProductPlan& p, Num num, Result res, hipStream_t s);
 void launch_product_grad(const ProductArgs& a, const ProductPlan& p, Num num, Pass pass, Result res, hipStream_t s);
 void launch_product_stream(const ProductArgs& a, Num num, Result res, hipStream_t s);
-void launch_product_join(const ProductArgs& a, Num num, Pass pass, Result res, hipStream_t s);
 void launch_quantize(int rows, int k, int type, const uint16_t* x, int64_t ldx, int8_t* codes, int64_t ldcodes,
                      float* scale, hipStream_t s);
 // (dg, du) [rows][2n] from dh [rows][n] and the saved (g, u)
