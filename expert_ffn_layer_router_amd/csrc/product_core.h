@@ -4,6 +4,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
 #include "products.h"
@@ -12,16 +13,14 @@ namespace moe {
 
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) void lds_any;
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-template <Num T> struct Acc { using t16 = f32x16; using t4 = f32x4; using t1 = float; };
-template <> struct Acc<Num::kInt8> { using t16 = i32x16; using t4 = i32x4; using t1 = int; };
+template <Num T> struct Acc { using t4 = f32x4; };
+template <> struct Acc<Num::kInt8> { using t4 = i32x4; };
 
 // Round to nearest even, NaN kept (hardware conversions).
 __device__ __forceinline__ uint32_t pack_f16_rne(float lo, float hi) {
@@ -73,20 +72,9 @@ __device__ __forceinline__ void activate_slope(int act, float g, float& value, f
   slope = fmaf(g * sig * rest, s.dz, sig) * unit;
 }
 
-// 32 x 32 of A (lane l: row l % 32, 16 bytes of the contraction at 16 (l / 32))
-// times B (the same for its columns): D holds column l % 32, rows
-// 8 (i / 4) + 4 (l / 32) + i % 4 in element i.
-template <Num T>
-__device__ __forceinline__ typename Acc<T>::t16 mfma32x32(u32x4 a, u32x4 b, typename Acc<T>::t16 c) {
-  if constexpr (T == Num::kBf16)
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-  else if constexpr (T == Num::kFp16)
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
-}
-// The same at 16 x 16 (lane l: row l % 16, 16 bytes at 16 (l / 16)): D holds
-// column l % 16, rows 4 (l / 16) + i.
+// 16 x 16 of A (lane l: row l % 16, 16 bytes of the contraction at
+// 16 (l / 16)) times B (the same for its columns): D holds column l % 16, rows
+// 4 (l / 16) + i.
 template <Num T>
 __device__ __forceinline__ typename Acc<T>::t4 mfma16x16(u32x4 a, u32x4 b, typename Acc<T>::t4 c) {
   if constexpr (T == Num::kBf16)
@@ -106,6 +94,14 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const char* base) {
 // 16 bytes per lane, global -> LDS: lane l writes dst + 16 l.
 __device__ __forceinline__ void buffer_to_lds16(__amdgpu_buffer_rsrc_t r, lds_char* dst, uint32_t voff, uint32_t soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_any*)dst, 16, voff, soff, 0, 0);
+}
+
+// Transposing LDS read.  `__restrict` (true here: nothing else is accessed in
+// the function) keeps the compiler from making the read wait for every copy
+// into LDS in flight; the stage's own copies are waited for explicitly.
+__device__ __forceinline__ u32x2 read_transposed(lds_char* __restrict p) {
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
 }
 
 // Waits for this wave's vector-memory operations, all but the newest N.
@@ -289,28 +285,32 @@ __device__ __forceinline__ bool find_row_tile(const ProductArgs& a, int tiles_n,
 //
 // JOIN: the block adds the raw sums of a split tile's parts, in order, instead
 // of computing them, and writes the result.
+constexpr int kRing = 5;  // LDS buffers of one operand's stage
 template <Num T, Pass PASS, Result RES, bool JOIN, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductArgs a) {
   constexpr int NW = WM * WN, THREADS = 64 * NW;
-  constexpr int MI = BM / 32 / WM, NJ = BN / 32 / WN;
+  constexpr int MI = BM / 16 / WM, NJ = BN / 16 / WN;
   constexpr bool P_STR = PASS == Pass::kWeightGrad, Q_STR = PASS != Pass::kForward;
   constexpr bool GATED = RES == Result::kGated;
   constexpr int ES = T == Num::kInt8 ? 1 : 2;
   constexpr int BK = 128 / ES;  // contraction values per stage
-  constexpr int kPBytes = BM * 128, kQBytes = BN * 128, kStage = kPBytes + kQBytes;
+  constexpr int kPBytes = BM * 128, kQBytes = BN * 128;
+  constexpr int kSlot = kPBytes;  // ring slot: one operand's stage
   constexpr int PI = kPBytes / 1024 / NW, QI = kQBytes / 1024 / NW;  // 1 KB copies per wave and stage
   constexpr int NO = GATED ? BN / 2 : BN;                            // result columns per block
+  static_assert(NJ <= MI && MI % PI == 0 && MI >= 4, "a read of Q and a copy of P per row block");
   static_assert(PI * NW * 1024 == kPBytes && QI * NW * 1024 == kQBytes, "even copy split");
-  static_assert(!GATED || (QI == 4 && NJ % 2 == 0), "a wave's copies of W lie in one block of 32 rows");
+  static_assert(!GATED || NJ % 2 == 0, "gate and up blocks in pairs");
   static_assert(T != Num::kInt8 || PASS == Pass::kForward, "codes have no backward pass");
-  using acc_t = typename Acc<T>::t16;
-  __shared__ __attribute__((aligned(1024))) char smem_raw[2 * kStage];
+  using acc_t = typename Acc<T>::t4;
+  __shared__ __attribute__((aligned(1024))) char smem_raw[kRing * kSlot];
+  static_assert(PI == QI && BM * BN * 2 <= kRing * kSlot, "equal slots; the 16-bit result fits the ring");
   lds_char* smem = (lds_char*)smem_raw;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int l32 = lane & 31, hh = lane >> 5;
+  const int l16 = lane & 15, quad = lane >> 4;
   const int F = a.cols / 2;  // gated: gate rows of W
   const int ncols = GATED ? F : a.cols;
   const int tiles_n = (ncols + NO - 1) / NO;
@@ -356,10 +356,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   const int stages = (klen + BK - 1) / BK;
   const int st0 = (int)((int64_t)stages * part / parts), st1 = (int)((int64_t)stages * (part + 1) / parts);
   // raw sums of a part: every lane's, 16 bytes each
-  auto raw = [&](int at, int i, int j, int q) {
-    using t4 = typename Acc<T>::t4;
-    return reinterpret_cast<t4*>(a.partial + (int64_t)at * (BM * BN * 4)) +
-           (((wave * MI + i) * NJ + j) * 4 + q) * 64 + lane;
+  auto raw = [&](int at, int i, int j) {
+    return reinterpret_cast<acc_t*>(a.partial + (int64_t)at * (BM * BN * 4)) + ((wave * MI + i) * NJ + j) * 64 + lane;
   };
 
   acc_t acc[MI][NJ];
@@ -372,13 +370,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const typename Acc<T>::t4 v = *raw(slot + s * slot_step, i, j, q);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
-          }
+        for (int j = 0; j < NJ; ++j) acc[i][j] += *raw(slot + s * slot_step, i, j);
   } else {
   // ---- copies ----
   const char* pbase = P_STR ? a.p + (int64_t)gbegin * a.ldp + (int64_t)row0 * ES : a.p + (int64_t)row0 * a.ldp;
@@ -389,9 +381,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
     qbase = a.q + (int64_t)group * a.q_group + (int64_t)n0 * ES;
   else
     qbase = a.q + (int64_t)gbegin * a.ldq + (int64_t)n0 * ES;
-  // gated: this wave copies 32 W rows, all gate or all up
-  const int qhalf = GATED ? (wave % NJ) % 2 : 0;
-  if (GATED && qhalf) qbase += (int64_t)F * a.ldq;
   uint32_t pv[PI], qv[QI];  // byte offsets of this lane's copies in stage 0, or kNoLoad
   int pk[PI], qk[QI];       // their contraction position: first value (contiguous) or row (strided)
   auto place = [&](bool strided, int j, int per_wave, int width, int64_t ld, int limit, bool gated, uint32_t& v, int& k) {
@@ -399,16 +388,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
     if (strided) {
       const int cpr = width / 8;  // 16-byte chunks per LDS row
       const int kr = inst * (64 / cpr) + lane / cpr;
-      const int c = (lane % cpr) ^ ((kr & 3) << 2);
+      const int c = (lane % cpr) ^ (((kr & 3) | ((kr >> 1) & 4)) << 1);
       v = 8 * c < limit ? (uint32_t)(kr * ld + 16 * c) : kNoLoad;
       k = kr;
     } else {
       const int r = inst * 8 + lane / 8;
       const int c = (lane & 7) ^ ((r >> 1) & 7);
       int src = r;
-      if (gated) {  // LDS row r: block r / 32 belongs to wave column (r / 32) / NJ
-        const int jb = r / 32;
-        src = (jb / NJ * (NJ / 2) + jb % NJ / 2) * 32 + r % 32;
+      if (gated) {  // LDS row r: block r / 16 belongs to wave column (r / 16) / NJ
+        const int jb = r / 16;
+        src = (jb / NJ * (NJ / 2) + jb % NJ / 2) * 16 + r % 16;
       }
       v = src < limit ? (uint32_t)(src * ld + 16 * c) : kNoLoad;
       k = c * (16 / ES);
@@ -418,118 +407,170 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   for (int j = 0; j < PI; ++j) place(P_STR, j, PI, BM, a.ldp, live, false, pv[j], pk[j]);
 #pragma unroll
   for (int j = 0; j < QI; ++j) place(Q_STR, j, QI, BN, a.ldq, ncols - n0, GATED, qv[j], qk[j]);
-  auto issue = [&](int st, int buf) {
-    lds_char* dst = smem + buf * kStage;
-    const int left = klen - st * BK;  // contraction values from this stage on
-    const __amdgpu_buffer_rsrc_t pr = buffer_at(P_STR ? pbase + (int64_t)st * BK * a.ldp : pbase + (int64_t)st * 128);
-    const __amdgpu_buffer_rsrc_t qr = buffer_at(Q_STR ? qbase + (int64_t)st * BK * a.ldq : qbase + (int64_t)st * 128);
-    if (left >= BK) {
+  // The copies of an operand's stage: begin_p / begin_q set the descriptor
+  // (and, in the contraction's last stage and past it, drop the lanes with
+  // nothing to load: in place, so that the copies' offsets live in registers
+  // of their own -- an offset in a temporary register makes the compiler wait
+  // for the copy before the register's next use), then copy_p(slot, c) is this
+  // wave's c-th copy into ring slot `slot`.
+  __amdgpu_buffer_rsrc_t pr, qr, ur;
+  auto values_from = [&](int st) { return st < st1 ? klen - st * BK : 0; };
+  auto begin_p = [&](int st) {
+    const int left = values_from(st);
+    if (left < BK) {
 #pragma unroll
-      for (int j = 0; j < PI; ++j) buffer_to_lds16(pr, dst + (wave * PI + j) * 1024, pv[j], 0);
-#pragma unroll
-      for (int j = 0; j < QI; ++j) buffer_to_lds16(qr, dst + kPBytes + (wave * QI + j) * 1024, qv[j], 0);
-    } else {
-#pragma unroll
-      for (int j = 0; j < PI; ++j)
-        buffer_to_lds16(pr, dst + (wave * PI + j) * 1024, pk[j] < left ? pv[j] : kNoLoad, 0);
-#pragma unroll
-      for (int j = 0; j < QI; ++j)
-        buffer_to_lds16(qr, dst + kPBytes + (wave * QI + j) * 1024, qk[j] < left ? qv[j] : kNoLoad, 0);
+      for (int j = 0; j < PI; ++j) pv[j] = pk[j] < left ? pv[j] : kNoLoad;
     }
+    pr = buffer_at(P_STR ? pbase + (int64_t)st * BK * a.ldp : pbase + (int64_t)st * 128);
+  };
+  auto begin_q = [&](int st) {
+    const int left = values_from(st);
+    if (left < BK) {
+#pragma unroll
+      for (int j = 0; j < QI; ++j) qv[j] = qk[j] < left ? qv[j] : kNoLoad;
+    }
+    const char* q = Q_STR ? qbase + (int64_t)st * BK * a.ldq : qbase + (int64_t)st * 128;
+    qr = buffer_at(q);
+    if (GATED) ur = buffer_at(q + (int64_t)F * a.ldq);
+  };
+  auto copy_p = [&](int slot, int c) { buffer_to_lds16(pr, smem + slot * kSlot + (wave * PI + c) * 1024, pv[c], 0); };
+  auto copy_q = [&](int slot, int c) {  // gated: the copy's 8 rows are gate or up
+    buffer_to_lds16(GATED && (wave * QI + c) / 2 % 2 ? ur : qr, smem + slot * kSlot + (wave * QI + c) * 1024, qv[c], 0);
   };
 
   // ---- fragments ----
-  // contiguous: lane l reads chunk 2s + hh of row (block row) + l % 32
-  const int row_at = l32 * 128, chunk_sw = (l32 >> 1) & 7;
-  // strided: lane 16g + j reads, for columns 16 (g % 2) + 4 (j % 4) .., row
-  // 16s + 8 (g / 2) + 4t + j / 4 (t = 0, 1)
-  const int sj = lane & 15, sg = lane >> 4;
+  // contiguous: lane l reads chunk 4s + l / 16 of row (block row) + l % 16
+  const int row_at = l16 * 128, chunk_sw = (l16 >> 1) & 7;
+  // strided: lane l reads, for columns 4 (l % 4) .. of its block, row
+  // 32s + 8 (l / 16) + 4t + l % 16 / 4 (t = 0, 1)
+  const int sj = l16 >> 2, fold = sj | (quad & 1) << 2;
   auto strided_at = [&](int width, int block) {
-    return (8 * (sg >> 1) + (sj >> 2)) * width * 2 + 64 * (block ^ (sj >> 2)) + 32 * (sg & 1) + 8 * (sj & 3);
+    return (8 * quad + sj) * width * 2 + 32 * (block ^ fold) + 8 * (l16 & 3);
   };
   int pat[MI], qat[NJ];
 #pragma unroll
-  for (int i = 0; i < MI; ++i) pat[i] = P_STR ? strided_at(BM, wm * MI + i) : (wm * MI + i) * 4096 + row_at;
+  for (int i = 0; i < MI; ++i) pat[i] = P_STR ? strided_at(BM, wm * MI + i) : (wm * MI + i) * 2048 + row_at;
 #pragma unroll
-  for (int j = 0; j < NJ; ++j)
-    qat[j] = kPBytes + (Q_STR ? strided_at(BN, wn * NJ + j) : (wn * NJ + j) * 4096 + row_at);
+  for (int j = 0; j < NJ; ++j) qat[j] = Q_STR ? strided_at(BN, wn * NJ + j) : (wn * NJ + j) * 2048 + row_at;
   auto fragment = [&](bool strided, int width, lds_char* at, int s) -> u32x4 {
     if (strided) {
-      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-      lds_char* q = at + s * 16 * width * 2;
-      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)q));
-      const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(q + 8 * width)));
+      lds_char* q = at + s * 32 * width * 2;
+      const u32x2 lo = read_transposed(q), hi = read_transposed(q + 8 * width);
       return u32x4{lo.x, lo.y, hi.x, hi.y};
     }
-    return *(__attribute__((address_space(3))) u32x4*)(at + 16 * ((2 * s + hh) ^ chunk_sw));
+    return *(__attribute__((address_space(3))) u32x4*)(at + 16 * ((4 * s + quad) ^ chunk_sw));
   };
-  auto read_step = [&](int buf, int s, u32x4(&pf)[MI], u32x4(&qf)[NJ]) {
-    lds_char* b = smem + buf * kStage;
+  // One row block's products.  The fences keep the order written here: each
+  // read and copy issues while products run.
+  u32x4 pf[MI], qf[2][NJ];
+  auto row = [&](int i, int step) {
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) qf[j] = fragment(Q_STR, BN, b + qat[j], s);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) pf[i] = fragment(P_STR, BM, b + pat[i], s);
-  };
-
-  auto products = [&](u32x4(&pf)[MI], u32x4(&qf)[NJ]) {
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = mfma32x32<T>(qf[j], pf[i], acc[i][j]);
+    for (int j = 0; j < NJ; ++j) acc[i][j] = mfma16x16<T>(qf[step][j], pf[i], acc[i][j]);
+    __builtin_amdgcn_sched_barrier(0);
   };
 
   const int nst = st1 - st0;
-  const bool busy = wm * MI * 32 < live;  // this wave has rows
+  const bool busy = wm * MI * 16 < live;  // this wave has rows
   if (nst > 0) {
-    issue(st0, 0);
-    wait_copies<0>();
-    lds_only_barrier();
-    if (nst > 1) issue(st0 + 1, 1);
-    u32x4 pf[2][MI], qf[2][NJ];
-    if (busy) {
-      read_step(0, 0, pf[0], qf[0]);
-      for (int i = 0; i < nst; ++i) {
-        const int buf = i & 1;
+    begin_p(st0);
 #pragma unroll
-        for (int s = 0; s < 3; ++s) {
-          read_step(buf, s + 1, pf[(s + 1) & 1], qf[(s + 1) & 1]);
-          products(pf[s & 1], qf[s & 1]);
+    for (int c = 0; c < PI; ++c) copy_p(0, c);
+    begin_q(st0);
+#pragma unroll
+    for (int c = 0; c < QI; ++c) copy_q(1, c);
+    begin_p(st0 + 1);
+#pragma unroll
+    for (int c = 0; c < PI; ++c) copy_p(2, c);
+    begin_q(st0 + 1);
+#pragma unroll
+    for (int c = 0; c < QI; ++c) copy_q(3, c);
+    wait_copies<PI + QI>();
+    lds_only_barrier();
+    // Iteration i: ps and qs hold stage i, pn and qn stage i + 1, `spare` is
+    // free and takes P's stage i + 2 during the first of the stage's two
+    // steps.  A quarter into the second step (all of stage i's fragments are
+    // in registers by then) every wave has to be done with stage i and stage
+    // i + 1 to have landed (that newest P may be in flight): ps takes Q's stage
+    // i + 2, and qs is the next spare one.  A row block's next P fragment
+    // replaces the current one as soon as its products are issued; Q's, which
+    // every row block uses, alternate between two sets.
+    int ps = 0, qs = 1, pn = 2, qn = 3, spare = 4;
+    auto turn = [&](int i) {
+      wait_copies<PI>();
+      lds_only_barrier();
+      begin_q(st0 + i + 2);
+    };
+    auto rotate = [&]() {
+      const int p = ps, q = qs;
+      ps = pn;
+      qs = qn;
+      pn = spare;
+      qn = p;
+      spare = q;
+    };
+    if (busy) {
+      constexpr int kHead = MI / 4;  // row blocks of the second step before the turn
+      auto read_p = [&](int slot, int i, int s) { pf[i] = fragment(P_STR, BM, smem + slot * kSlot + pat[i], s); };
+      auto read_q = [&](int slot, int j, int s) { qf[s][j] = fragment(Q_STR, BN, smem + slot * kSlot + qat[j], s); };
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) read_q(qs, j, 0);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) read_p(ps, i, 0);
+      for (int i = 0; i < nst; ++i) {
+        begin_p(st0 + i + 2);
+#pragma unroll
+        for (int m = 0; m < MI; ++m) {
+          row(m, 0);
+          read_p(ps, m, 1);
+          if (m < NJ) read_q(qs, m, 1);
+          if (m % (MI / PI) == 0) copy_p(spare, m / (MI / PI));
         }
-        if (i + 1 < nst) {
-          wait_copies<0>();
-          lds_only_barrier();
-          if (i + 2 < nst) issue(st0 + i + 2, buf);
-          read_step(buf ^ 1, 0, pf[0], qf[0]);
+#pragma unroll
+        for (int m = 0; m < kHead; ++m) row(m, 1);
+        turn(i);
+#pragma unroll
+        for (int m = 0; m < kHead; ++m) read_p(pn, m, 0);
+#pragma unroll
+        for (int m = kHead; m < MI; ++m) {
+          constexpr int kRest = MI - kHead;
+          row(m, 1);
+          read_p(pn, m, 0);
+#pragma unroll
+          for (int j = NJ * (m - kHead) / kRest; j < NJ * (m - kHead + 1) / kRest; ++j) read_q(qn, j, 0);
+#pragma unroll
+          for (int c = QI * (m - kHead) / kRest; c < QI * (m - kHead + 1) / kRest; ++c) copy_q(ps, c);
         }
-        products(pf[1], qf[1]);
+        rotate();
       }
     } else {
       // a wave without rows only copies
-      for (int i = 0; i + 1 < nst; ++i) {
-        wait_copies<0>();
-        lds_only_barrier();
-        if (i + 2 < nst) issue(st0 + i + 2, i & 1);
+      for (int i = 0; i < nst; ++i) {
+        begin_p(st0 + i + 2);
+#pragma unroll
+        for (int c = 0; c < PI; ++c) copy_p(spare, c);
+        turn(i);
+#pragma unroll
+        for (int c = 0; c < QI; ++c) copy_q(ps, c);
+        rotate();
       }
     }
+    wait_copies<0>();  // the zeros of stages past the end
   }
-
   if (parts > 1) {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *raw(slot, i, j, q) = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+      for (int j = 0; j < NJ; ++j) *raw(slot, i, j) = acc[i][j];
     return;
   }
   }  // !JOIN
 
   // ---- results ----
-  // element e of acc[i][j]: row rowl(i), column coll(j) + 8 (e / 4) + e % 4
-  auto rowl = [&](int i) { return (wm * MI + i) * 32 + l32; };
+  // element e of acc[i][j]: row rowl(i), column coll(j) + e
+  auto rowl = [&](int i) { return (wm * MI + i) * 16 + l16; };
   auto coll = [&](int j) {
-    return (GATED ? (wn * (NJ / 2) + j / 2) * 32 : (wn * NJ + j) * 32) + 4 * hh;
+    return (GATED ? (wn * (NJ / 2) + j / 2) * 16 : (wn * NJ + j) * 16) + 4 * quad;
   };
   {
     const bool fp16 = T == Num::kFp16 || (T == Num::kInt8 && a.out_type == MOE_TYPE_FP16);
@@ -540,16 +581,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
       for (int i = 0; i < MI; ++i) prow[i] = rowl(i) < live ? a.pscale[row0 + rowl(i)] : 0.0f;
     }
     const float* qs = T == Num::kInt8 ? a.qscale + (int64_t)group * a.cols : nullptr;
-    auto value = [&](int i, int j, int q) -> f32x4 {
+    auto value = [&](int i, int j) -> f32x4 {
       f32x4 v;
       if constexpr (T == Num::kInt8) {
-        const int c = n0 + coll(j) + 8 * q;
+        const int c = n0 + coll(j);
         const f32x4 s = c < ncols ? *reinterpret_cast<const f32x4*>(qs + c + (GATED && j % 2 ? F : 0)) : f32x4{};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][j][4 * q + e] * prow[i] * s[e];
+        for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][j][e] * prow[i] * s[e];
       } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
+        v = acc[i][j];
       }
       return v;
     };
@@ -561,12 +601,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
         if (rowl(i) >= live) continue;
         char* rowp = outp + ((int64_t)row0 + rowl(i)) * a.ldout * 4;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int c = n0 + coll(j) + 8 * q;
-            if (c < ncols) *reinterpret_cast<f32x4*>(rowp + (int64_t)c * 4) = value(i, j, q);
-          }
+        for (int j = 0; j < NJ; ++j) {
+          const int c = n0 + coll(j);
+          if (c < ncols) *reinterpret_cast<f32x4*>(rowp + (int64_t)c * 4) = value(i, j);
+        }
       }
     } else {
       uint16_t* outp = (uint16_t*)a.out;
@@ -584,17 +622,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < NJ; j += GATED ? 2 : 1)
+        for (int j = 0; j < NJ; j += GATED ? 2 : 1) {
+          f32x4 v = value(i, j);
+          if constexpr (GATED) {
+            const f32x4 u = value(i, j + 1);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            f32x4 v = value(i, j, q);
-            if constexpr (GATED) {
-              const f32x4 u = value(i, j + 1, q);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] = activate(a.act, v[e]) * u[e];
-            }
-            put(NO, rowl(i), coll(j) + 8 * q, v);
+            for (int e = 0; e < 4; ++e) v[e] = activate(a.act, v[e]) * u[e];
           }
+          put(NO, rowl(i), coll(j), v);
+        }
       __syncthreads();
       for (int x = tid; x < BM * (NO / 8); x += THREADS) {
         const int r = x / (NO / 8), c = x % (NO / 8);
@@ -608,9 +644,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
 #pragma unroll
           for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-              for (int q = 0; q < 4; ++q) put(BN, rowl(i), coll(j) + 8 * q + (j % 2 ? NO : 0), value(i, j, q));
+            for (int j = 0; j < NJ; ++j) put(BN, rowl(i), coll(j) + (j % 2 ? NO : 0), value(i, j));
           __syncthreads();
           for (int x = tid; x < BM * (BN / 8); x += THREADS) {
             const int r = x / (BN / 8), c = x % (BN / 8);
