@@ -67,8 +67,8 @@ def test_workspace_holds_the_slopes_and_the_parts(lib):
     # a few rows past the streaming kernel and a narrow result: the contraction is split
     st, n = workspace(lib, "expert_product", rows=100, n=128, k=8192)
     assert st == 0 and n > 0
-    # many blocks: no split
-    assert workspace(lib, "expert_product", rows=4096, n=8192, k=4096) == (0, 0)
+    # sums too short to split
+    assert workspace(lib, "expert_product", rows=4096, n=8192, k=256) == (0, 0)
     assert workspace(lib, "expert_product", rows=0, n=128, k=8192) == (0, 0)
     # the largest shapes stay in range of the size type
     st, n = workspace(lib, "gated_product_backward", rows=1 << 22, n=32768, k=65536, groups=256)
