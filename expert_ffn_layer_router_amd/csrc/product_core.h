@@ -465,8 +465,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   u32x4 pf[MI], qf[2][NJ];
   auto row = [&](int i, int step) {
     __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = mfma16x16<T>(qf[step][j], pf[i], acc[i][j]);
+    __builtin_amdgcn_s_setprio(0);
     __builtin_amdgcn_sched_barrier(0);
   };
 
@@ -489,7 +491,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
     lds_only_barrier();
     // Iteration i: ps and qs hold stage i, pn and qn stage i + 1, `spare` is
     // free and takes P's stage i + 2 during the first of the stage's two
-    // steps.  A quarter into the second step (all of stage i's fragments are
+    // steps.  Three eighths into the second step (all of stage i's fragments are
     // in registers by then) every wave has to be done with stage i and stage
     // i + 1 to have landed (that newest P may be in flight): ps takes Q's stage
     // i + 2, and qs is the next spare one.  A row block's next P fragment
@@ -510,7 +512,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
       spare = q;
     };
     if (busy) {
-      constexpr int kHead = MI / 4;  // row blocks of the second step before the turn
+      constexpr int kHead = MI * 3 / 8;  // row blocks of the second step before the turn
       auto read_p = [&](int slot, int i, int s) { pf[i] = fragment(P_STR, BM, smem + slot * kSlot + pat[i], s); };
       auto read_q = [&](int slot, int j, int s) { qf[s][j] = fragment(Q_STR, BN, smem + slot * kSlot + qat[j], s); };
 #pragma unroll
