@@ -1,15 +1,15 @@
-// Grouped products of few rows (up to 64 in the call): bound by reading each
-// used group's weights once.
+// Grouped products of few rows per group: bound by reading each used group's
+// weights once.
 //
 // A block owns 16 NC columns of one group (gated: 16 gate and the same 16 up
-// columns) and all of the group's rows, in up to MT tiles of 16.  Its 8 waves
-// take the contraction's 64-byte steps (32 16-bit values, 64 codes) in runs of
-// kRun, dealt round-robin, and read w straight into registers: the weights
-// pass the compute unit once and nothing is reused through LDS.  kRun steps
-// of loads are in flight per wave while the previous ones are multiplied.
-// The rows come from the caches in the same fragment layout.  The waves' sums
-// meet in LDS and are added in wave order, so the result does not depend on
-// timing.
+// columns) and up to 16 MT of the group's rows.  Its 4 waves each take a
+// quarter of the contraction, in 64-byte steps (32 16-bit values, 64 codes),
+// and read w straight into registers: the weights pass the compute unit once
+// and nothing is reused through LDS.  kRun steps are loaded while the previous
+// kRun are multiplied; a wave's steps are consecutive, so that it reads
+// kilobytes of each row in turn.  The rows come from the caches in the same
+// fragment layout.  The waves' sums meet in LDS and are added in wave order, so
+// the result does not depend on timing.
 #include <type_traits>
 
 #include "product_core.h"
@@ -18,15 +18,14 @@ namespace moe {
 
 namespace {
 
-constexpr int kStreamWaves = 8;
-constexpr int kRun = 4;  // 64-byte steps in flight per wave
+constexpr int kStreamWaves = 4;
 
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
 }
 
 template <Num T, Result RES, int MT, int NC>
-__global__ __launch_bounds__(64 * kStreamWaves, MT >= 4 ? 2 : 4) void product_stream_kernel(ProductArgs a) {
+__global__ __launch_bounds__(64 * kStreamWaves, MT == 4 ? 2 : 4) void product_stream_kernel(ProductArgs a) {
   constexpr bool GATED = RES == Result::kGated;
   static_assert(!GATED || NC == 2, "a gated block holds one gate and one up tile");
   constexpr int ES = T == Num::kInt8 ? 1 : 2;
@@ -36,9 +35,9 @@ __global__ __launch_bounds__(64 * kStreamWaves, MT >= 4 ? 2 : 4) void product_st
   const int group = blockIdx.y;
   int begin, end;
   group_rows(a.offsets, a.rows, group, begin, end);
-  const int live = __builtin_amdgcn_readfirstlane(end - begin);
+  begin = __builtin_amdgcn_readfirstlane(begin) + blockIdx.z * 16 * MT;
+  const int live = min(16 * MT, __builtin_amdgcn_readfirstlane(end) - begin);
   if (live <= 0) return;
-  begin = __builtin_amdgcn_readfirstlane(begin);
   const int F = a.cols / 2, ncols = GATED ? F : a.cols;
   const int n0 = blockIdx.x * NO;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -65,29 +64,44 @@ __global__ __launch_bounds__(64 * kStreamWaves, MT >= 4 ? 2 : 4) void product_st
 #pragma unroll
     for (int c = 0; c < NC; ++c) acc[m][c] = acc_t{};
 
-  const int bytes = a.contract * ES;  // of a row; a multiple of 16
+  const int bytes = a.contract * ES;  // of a row
   const int steps = (bytes + 63) / 64;
   // the row tiles in use are a compile-time count, so that the loop holds no branches
   auto body = [&](auto tag) {
     constexpr int ML = decltype(tag)::value;
-    u32x4 w0[kRun][NC], x0[kRun][ML];
-    for (int s0 = wave * kRun; s0 < steps; s0 += kStreamWaves * kRun) {
-      const uint32_t at = (uint32_t)s0 * 64;
-      const bool whole = s0 * 64 + kRun * 64 <= bytes;
+    constexpr int kRun = ML == 1 ? 4 : 2;  // steps loaded together, as the registers allow
+    // this wave's steps [s, s1): contiguous, so that a wave reads long runs of
+    // each row
+    const int s1 = (int)((int64_t)steps * (wave + 1) / kStreamWaves);
+    int s = (int)((int64_t)steps * wave / kStreamWaves);
+    u32x4 w[2][kRun][NC], x[2][kRun][ML];
+    auto load = [&](int b, int at) {
 #pragma unroll
       for (int u = 0; u < kRun; ++u) {
-        const bool in = whole || s0 * 64 + u * 64 + 16 * quad < bytes;
+        const bool in = (at + u) * 64 + 16 * quad < bytes && at + u < s1;  // bytes: a multiple of 16
 #pragma unroll
-        for (int c = 0; c < NC; ++c) w0[u][c] = load16(wr[c], in ? wv[c] : kNoLoad, at + u * 64);
+        for (int c = 0; c < NC; ++c) w[b][u][c] = load16(wr[c], in ? wv[c] : kNoLoad, (uint32_t)(at + u) * 64);
 #pragma unroll
-        for (int m = 0; m < ML; ++m) x0[u][m] = load16(xr, in ? xv[m] : kNoLoad, at + u * 64);
+        for (int m = 0; m < ML; ++m) x[b][u][m] = load16(xr, in ? xv[m] : kNoLoad, (uint32_t)(at + u) * 64);
       }
+    };
+    auto multiply = [&](int b) {
 #pragma unroll
       for (int u = 0; u < kRun; ++u)
 #pragma unroll
         for (int m = 0; m < ML; ++m)
 #pragma unroll
-          for (int c = 0; c < NC; ++c) acc[m][c] = mfma16x16<T>(w0[u][c], x0[u][m], acc[m][c]);
+          for (int c = 0; c < NC; ++c) acc[m][c] = mfma16x16<T>(w[b][u][c], x[b][u][m], acc[m][c]);
+    };
+    if (s < s1) load(0, s);
+    while (s < s1) {
+      if (s + kRun < s1) load(1, s + kRun);
+      multiply(0);
+      s += kRun;
+      if (s >= s1) break;
+      if (s + kRun < s1) load(0, s + kRun);
+      multiply(1);
+      s += kRun;
     }
   };
   const int tiles = (live + 15) / 16;
@@ -107,42 +121,42 @@ __global__ __launch_bounds__(64 * kStreamWaves, MT >= 4 ? 2 : 4) void product_st
   // lane l of tile (m, c): row 16m + l % 16, columns 16c + 4 (l / 16) ..
   const bool fp16 = T == Num::kFp16 || (T == Num::kInt8 && a.out_type == MOE_TYPE_FP16);
   constexpr int kTiles = GATED ? MT : MT * NC;  // result tiles
-  if (wave >= kTiles) return;
-  static_assert(kTiles <= kStreamWaves, "one wave per result tile");
-  const int m = GATED ? wave : wave / NC, c = GATED ? 0 : wave % NC;
-  const int row = 16 * m + l16, col = n0 + 16 * c + 4 * quad;
-  if (row >= live || col >= ncols) return;
-  auto total = [&](int tile, int up) -> f32x4 {
-    acc_t v = part[0][tile][lane];
+  for (int tile = wave; tile < kTiles; tile += kStreamWaves) {
+    const int m = GATED ? tile : tile / NC, c = GATED ? 0 : tile % NC;
+    const int row = 16 * m + l16, col = n0 + 16 * c + 4 * quad;
+    if (row >= live || col >= ncols) continue;
+    auto total = [&](int t, int up) -> f32x4 {
+      acc_t v = part[0][t][lane];
 #pragma unroll
-    for (int w = 1; w < kStreamWaves; ++w) v += part[w][tile][lane];
-    f32x4 f;
-    if constexpr (T == Num::kInt8) {
-      const float ps = a.pscale[begin + row];
-      const f32x4 s = *reinterpret_cast<const f32x4*>(a.qscale + (int64_t)group * a.cols + (up ? F : 0) + col);
+      for (int w = 1; w < kStreamWaves; ++w) v += part[w][t][lane];
+      f32x4 f;
+      if constexpr (T == Num::kInt8) {
+        const float ps = a.pscale[begin + row];
+        const f32x4 s = *reinterpret_cast<const f32x4*>(a.qscale + (int64_t)group * a.cols + (up ? F : 0) + col);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] = (float)v[e] * ps * s[e];
-    } else {
-      f = v;
-    }
-    return f;
-  };
-  if constexpr (RES == Result::kWide) {
-    *reinterpret_cast<f32x4*>((float*)a.out + (int64_t)(begin + row) * a.ldout + col) = total(wave, 0);
-  } else {
-    f32x4 v = total(GATED ? m * NC : wave, 0);
-    if constexpr (GATED) {
-      const f32x4 u = total(m * NC + 1, 1);
-      if (T != Num::kInt8 && a.keep) {
-        uint16_t* k = a.keep + (int64_t)(begin + row) * a.ldkeep + col;
-        *reinterpret_cast<u32x2*>(k) = u32x2{pack_half(fp16, v[0], v[1]), pack_half(fp16, v[2], v[3])};
-        *reinterpret_cast<u32x2*>(k + F) = u32x2{pack_half(fp16, u[0], u[1]), pack_half(fp16, u[2], u[3])};
+        for (int e = 0; e < 4; ++e) f[e] = (float)v[e] * ps * s[e];
+      } else {
+        f = v;
       }
+      return f;
+    };
+    f32x4 v = total(GATED ? m * NC : tile, 0);
+    if constexpr (RES == Result::kWide) {
+      *reinterpret_cast<f32x4*>((float*)a.out + (int64_t)(begin + row) * a.ldout + col) = v;
+    } else {
+      if constexpr (GATED) {
+        const f32x4 u = total(m * NC + 1, 1);
+        if (T != Num::kInt8 && a.keep) {
+          uint16_t* k = a.keep + (int64_t)(begin + row) * a.ldkeep + col;
+          *reinterpret_cast<u32x2*>(k) = u32x2{pack_half(fp16, v[0], v[1]), pack_half(fp16, v[2], v[3])};
+          *reinterpret_cast<u32x2*>(k + F) = u32x2{pack_half(fp16, u[0], u[1]), pack_half(fp16, u[2], u[3])};
+        }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = activate(a.act, v[e]) * u[e];
+        for (int e = 0; e < 4; ++e) v[e] = activate(a.act, v[e]) * u[e];
+      }
+      *reinterpret_cast<u32x2*>((uint16_t*)a.out + (int64_t)(begin + row) * a.ldout + col) =
+          u32x2{pack_half(fp16, v[0], v[1]), pack_half(fp16, v[2], v[3])};
     }
-    *reinterpret_cast<u32x2*>((uint16_t*)a.out + (int64_t)(begin + row) * a.ldout + col) =
-        u32x2{pack_half(fp16, v[0], v[1]), pack_half(fp16, v[2], v[3])};
   }
 }
 
@@ -150,19 +164,28 @@ template <Num T, Result RES, int NC>
 void launch_mt(const ProductArgs& a, hipStream_t s) {
   const int ncols = RES == Result::kGated ? a.cols / 2 : a.cols;
   const int no = RES == Result::kGated ? 16 : 16 * NC;
-  const dim3 grid((ncols + no - 1) / no, a.groups);
+  // row tiles of 16 of the largest possible group, up to 4 a block
+  const int mt = a.rows <= 16 ? 1 : a.rows <= 32 ? 2 : 4;
+  const dim3 grid((ncols + no - 1) / no, a.groups, (a.rows + 16 * mt - 1) / (16 * mt));
   const int threads = 64 * kStreamWaves;
-  if (a.rows <= 16)
+  if (mt == 1)
     product_stream_kernel<T, RES, 1, NC><<<grid, threads, 0, s>>>(a);
-  else if (a.rows <= 32)
+  else if (mt == 2)
     product_stream_kernel<T, RES, 2, NC><<<grid, threads, 0, s>>>(a);
   else
     product_stream_kernel<T, RES, 4, NC><<<grid, threads, 0, s>>>(a);
 }
 
+// A block of 32 columns reads the rows half as often, one of 16 makes twice as
+// many blocks: 96 rows over 64 groups of 4096 columns of 2048 (8192 blocks of
+// 32): 92 against 106 us; 16 rows x one group of 4096 columns of 14336 (128
+// blocks): 45 against 34 us; 1024 blocks: within 2%.
+constexpr int kWideBlocks = 2048;
 template <Num T, Result RES>
 void launch_stream(const ProductArgs& a, hipStream_t s) {
   if constexpr (RES == Result::kGated)
+    launch_mt<T, RES, 2>(a, s);
+  else if ((int64_t)a.groups * ((a.cols + 31) / 32) >= kWideBlocks)
     launch_mt<T, RES, 2>(a, s);
   else
     launch_mt<T, RES, 1>(a, s);
