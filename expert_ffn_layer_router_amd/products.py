@@ -23,6 +23,7 @@ from . import _lib
 ACTIVATIONS = {"silu": _lib.MOE_ACT_SILU, "gelu": _lib.MOE_ACT_GELU}
 
 
+@lru_cache(maxsize=None)
 def _torch():
     import torch
     return torch
@@ -69,59 +70,61 @@ def _act(name) -> int:
 class _Call:
     """Checks the tensors of one call against each other, finds its stream and
     makes the calling thread's device and stream match while it allocates and
-    enqueues."""
+    enqueues.  (Short calls are bound by the host: the checks are ordered so
+    that what is right costs one comparison each.)"""
+
+    __slots__ = ("lib", "index", "device", "guards", "stream")
 
     def __init__(self, first, stream):
-        torch = _torch()
+        cuda = _torch().cuda
         self.lib = _lib.load()
-        if not first.is_cuda:
+        self.index = first.get_device()
+        if self.index < 0:
             raise ValueError("the tensors must be on a GPU")
         self.device = first.device
-        self._guards = []
-        if torch.cuda.current_device() != self.device.index:
-            self._guards.append(torch.cuda.device(self.device))
+        self.guards = ()
+        if cuda.current_device() != self.index:
+            self.guards = (cuda.device(self.index),)
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
+            self.stream = cuda.current_stream(self.index).cuda_stream
         else:
             if stream.device != self.device:
                 raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
-            self._guards.append(torch.cuda.stream(stream))
-        self.stream = ctypes.c_void_p(stream.cuda_stream)
+            self.guards += (cuda.stream(stream),)
+            self.stream = stream.cuda_stream
 
     def __enter__(self):
-        for g in self._guards:
+        for g in self.guards:
             g.__enter__()
         return self
 
     def __exit__(self, *exc):
-        for g in reversed(self._guards):
+        for g in reversed(self.guards):
             g.__exit__(*exc)
 
     def rows(self, name, t, rows, width, dtype):
         """(pointer, row stride) of a [rows, width] matrix."""
-        self.same_device(name, t)
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-        if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
-            raise ValueError(f"{name} must be [{rows}, {width}], not {list(t.shape)}")
-        if t.stride(1) != 1:
+        if t.shape != (rows, width) or t.dtype is not dtype or t.get_device() != self.index:
+            self.refuse(name, t, (rows, width), dtype)
+        stride, one = t.stride()
+        if one != 1:
             raise ValueError(f"the values of a row of {name} must be contiguous")
-        return t.data_ptr(), (t.stride(0) if rows > 1 else width)
+        return t.data_ptr(), (stride if rows > 1 else width)
 
     def plain(self, name, t, shape, dtype):
         """Pointer of a contiguous tensor."""
-        self.same_device(name, t)
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != self.index:
+            self.refuse(name, t, shape, dtype)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr()
 
-    def same_device(self, name, t):
+    def refuse(self, name, t, shape, dtype):
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, not on {self.device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
 
     def offsets(self, offsets, groups):
         if offsets is None:
@@ -135,7 +138,8 @@ class _Call:
                 return None, 0, None
             workspace = _torch().empty(need, dtype=_torch().uint8, device=self.device)
         else:
-            self.same_device("workspace", workspace)
+            if workspace.get_device() != self.index:
+                raise ValueError(f"workspace is on {workspace.device}, not on {self.device}")
             if not workspace.is_contiguous():
                 raise ValueError("workspace must be contiguous")
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
@@ -143,6 +147,7 @@ class _Call:
     def result(self, name, out, rows, width, dtype):
         if out is None:
             out = _torch().empty((rows, width), dtype=dtype, device=self.device)
+            return out, out.data_ptr(), width
         return (out, *self.rows(name, out, rows, width, dtype))
 
 
