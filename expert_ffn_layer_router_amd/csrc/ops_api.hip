@@ -15,15 +15,24 @@ namespace {
 
 constexpr int kMaxRows = 1 << 22, kMaxWidth = 65536, kMaxGroups = 256;
 constexpr int64_t kMaxStride = 1 << 20;
-// The streaming kernel takes calls of up to 16 rows, and of up to 8 rows per
-// group on average: reading the used groups' weights is then all the time, and
-// it reads them faster than the tiles do, whose rows are mostly padding
-// (16 rows x one group of 6400 gated columns of 4096 in bf16: 29.6 against 38.4
-// us; 384 rows over 64 groups of 2048 gated columns: 376 against 562 us).  With
-// more rows in a group each block reads them again and again (24 rows x the
-// one group above: 70 against 37 us; 128 rows over 16 groups: within 20% of
-// each other either way).
-constexpr int kStreamRows = 16, kStreamGroupRows = 8;
+// The streaming kernel takes calls with up to 16 rows per group on average:
+// reading the used groups' weights is then most of the time, and it reads them
+// faster than the tiles do, whose rows are mostly padding (16 rows x one group
+// of 6400 gated columns of 4096 in bf16: 29.6 against 38.4 us; 256 rows over
+// 16 groups of 2048: 106 against 166; 384 over 64: 376 against 562; uneven
+// groups cost it: 128 rows over 16 groups of 4096 columns of 6400, 47 in the
+// largest: 194 against 158).
+constexpr int kStreamGroupRows = 16;
+// With more rows its blocks read them over and over (and the weights once for
+// every 64 rows of a group), which still beats the tiles' fixed costs, a
+// second kernel for the split contraction among them, while it is little and
+// the groups and rows are not long enough to fill the chip with tiles: 64 rows
+// x 4096 columns of 2048 codes: 8.9 against 16.1 us; 100 rows x 2048 gated
+// columns of 2048 in bf16: 15.8 against 22.1; 256 x 1024 of 2048: 13.2 against
+// 20.6; 64 x the 6400 columns (210 MB of rows): 53 against 38; 300 x 128 of
+// 8192: 39 against 23; 2048 x 512 of 512: 13.6 against 10.1.
+constexpr int64_t kStreamExtraBytes = 48 << 20;
+constexpr int kStreamExtraRows = 512, kStreamExtraRowBytes = 8192;
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -32,11 +41,18 @@ size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
 ProductPlan plan_product(Num num, Pass pass, Result res, const ProductArgs& a) {
   ProductPlan p;
-  if (pass == Pass::kForward && a.rows <= std::max(kStreamRows, kStreamGroupRows * a.groups)) {
-    p.family = Family::kStream;
-    return p;
-  }
   const bool gated = res == Result::kGated, wg = pass == Pass::kWeightGrad;
+  if (pass == Pass::kForward) {
+    const int64_t row_bytes = (int64_t)a.contract * (num == Num::kInt8 ? 1 : 2);
+    const int64_t row_reads = (int64_t)(a.cols / (gated ? 32 : 16) + 1) * a.rows * row_bytes;
+    const int64_t weight_reads = (a.rows - 1) / (64 * a.groups) * ((int64_t)a.groups * a.cols * row_bytes);
+    if (a.rows <= kStreamGroupRows * a.groups ||
+        (a.rows <= kStreamExtraRows * a.groups && row_bytes <= kStreamExtraRowBytes &&
+         (row_reads + weight_reads) / 2 <= kStreamExtraBytes)) {
+      p.family = Family::kStream;
+      return p;
+    }
+  }
   // rows of an average group: the tiles' rows, or in the weight gradient the
   // contraction; the offsets themselves are on the device
   const int group_rows = std::max(1, ceil_div(a.rows, a.groups));
@@ -61,7 +77,7 @@ ProductPlan plan_product(Num num, Pass pass, Result res, const ProductArgs& a) {
     // the most parts of a tile that can pay (rounds_of)
     const int64_t tiles = (int64_t)row_tile_bound(a.rows, a.groups, tile) * ceil_div(cols, gated ? tile / 2 : tile);
     p.splits = std::max(1, std::min(8, stages / 4));
-    if (stages * (p.splits - 1) / p.splits <= 6) p.splits = 1;
+    if (stages * (p.splits - 1) / p.splits <= (large ? 6 : 12)) p.splits = 1;
     units = split_units(tile, (int)std::min<int64_t>(tiles, 1 << 20), p.splits);
   }
   if (p.splits > 1) p.partial_bytes = units * tile * tile * 4;

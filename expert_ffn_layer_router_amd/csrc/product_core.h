@@ -159,7 +159,7 @@ __host__ __device__ __forceinline__ Rounds rounds_of(int tiles, int stages, int 
     int s = slots / r.rem;
     s = s < max_parts ? s : max_parts;
     s = s < stages / 4 ? s : stages / 4;
-    const int cost = BM == 256 ? 6 + r.rem * s / 8 : 6 + r.rem * s / 32;  // in stages
+    const int cost = BM == 256 ? 6 + r.rem * s / 8 : 12 + r.rem * s / 32;  // in stages
     if (s > 1 && stages * (s - 1) / s > cost) r.parts = s;
   }
   return r;

@@ -121,7 +121,10 @@ FEW = [([1], 8, 8), ([1], 64, 4096), ([3], 1000, 72), ([16], 40, 136), ([17], 24
        ([64], 128, 520), ([0, 1, 0, 5, 16, 0, 7], 72, 200), ([20, 0, 44], 136, 328)]
 TILES = [([65], 8, 8), ([129], 136, 72), ([200], 1000, 1416), ([0, 70, 0, 1, 128, 255, 0], 264, 200),
          ([256, 300], 128, 64), ([1000], 392, 456), ([3, 130, 67], 1000, 2056)]
-BIG = [([4096], 4096, 72), ([511, 0, 1300, 257, 700, 130], 2568, 136)]  # enough tiles for the 256-wide blocks
+# past the streaming kernel: 128-wide blocks (whole, and with the contraction split), 256-wide ones (the
+# remainder of the last round split in the last)
+BIG = [([3700], 4096, 72), ([500, 0, 1, 1255, 129, 1100], 1000, 2056), ([2049], 520, 4104), ([4096], 4096, 72),
+       ([511, 0, 1300, 257, 700, 130], 2568, 136), ([3000, 1, 900], 4104, 4104)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -136,7 +139,7 @@ def test_expert_product(torch, moe, sizes, n, k, dtype):
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("sizes,n,k", FEW + TILES + [BIG[1]], ids=str)
+@pytest.mark.parametrize("sizes,n,k", FEW + TILES + BIG[1:], ids=str)
 def test_gated_product(torch, moe, sizes, n, k, dtype, act):
     say(f"gated_product {sizes} {n} {k} {dtype} {act}")
     c = Case(torch, sizes, n, k, getattr(torch, dtype), wide=2)
@@ -195,7 +198,7 @@ def slopes64(torch, act, dh, gu, n, dtype):
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("sizes,n,k", FEW + TILES + [BIG[1]], ids=str)
+@pytest.mark.parametrize("sizes,n,k", FEW + TILES + BIG[1:], ids=str)
 def test_gated_product_backward(torch, moe, sizes, n, k, dtype, act):
     say(f"gated_product_backward {sizes} {n} {k} {dtype} {act}")
     c = Case(torch, sizes, n, k, getattr(torch, dtype), wide=2)
@@ -334,7 +337,7 @@ def strided(torch, t, pad, fill):
     return buf, buf[:, :t.shape[1]]
 
 
-@pytest.mark.parametrize("sizes,n,k", [([5, 0, 9], 72, 208), ([100, 0, 150, 3], 264, 208), ([2000, 1500], 2560, 80)],
+@pytest.mark.parametrize("sizes,n,k", [([5, 0, 9], 72, 208), ([100, 0, 150, 3], 264, 208), ([1500, 0, 700, 3], 520, 4112), ([2000, 1500], 2560, 80)],
                          ids=str)
 def test_rows_of_no_group_and_strides(torch, moe, sizes, n, k):
     """Rows before and behind the groups hold NaN and are neither read nor written, nor is the space between rows."""
@@ -404,7 +407,7 @@ def test_rows_of_no_group_and_strides(torch, moe, sizes, n, k):
     check(torch, out[m], ref[m], rounded(torch, ref, 3 * E * ref.abs(), torch.float32)[m], "int8")
 
 
-@pytest.mark.parametrize("rows", [5, 300])
+@pytest.mark.parametrize("rows", [5, 300, 5000])
 def test_nonfinite_values_stay_in_their_row_and_group(torch, moe, rows):
     c = Case(torch, [rows, rows], 72, 136, torch.bfloat16)
     c.x[1, 5] = float("nan")
@@ -495,7 +498,7 @@ def test_gradients_against_differences(torch, moe, act):
 
 # ---- how the calls are used --------------------------------------------------------
 
-def every_call(torch, moe, rows=300, n=264, k=208, seed=0, t=None):
+def every_call(torch, moe, rows, n, k, seed=0, t=None):
     """(name, function of no arguments returning tensors) for each operator."""
     t = t or torch.bfloat16
     sizes = [rows // 3, 0, rows - rows // 3]
@@ -520,7 +523,7 @@ def tensors(out):
     return list(out) if isinstance(out, tuple) else [out]
 
 
-@pytest.mark.parametrize("rows", [7, 300])
+@pytest.mark.parametrize("rows", [7, 300, 2500])
 def test_same_call_same_bits_on_any_stream(torch, moe, rows):
     side = torch.cuda.Stream()
     for name, call in every_call(torch, moe, rows, n=128, k=4096):  # few blocks: split contractions
@@ -534,7 +537,7 @@ def test_same_call_same_bits_on_any_stream(torch, moe, rows):
             assert torch.equal(a, b) and torch.equal(a, c), name
 
 
-@pytest.mark.parametrize("rows", [7, 300])
+@pytest.mark.parametrize("rows", [7, 300, 2500])
 def test_captured_calls_replay(torch, moe, rows):
     """Each call captured into a graph with its buffers; replays follow rewritten inputs, with eager work between."""
     for index, (name, call) in enumerate(every_call(torch, moe, rows, n=128, k=4096)):
@@ -556,12 +559,13 @@ def test_captured_calls_replay(torch, moe, rows):
 
 def test_two_graphs_share_a_workspace(torch, moe):
     """Graphs over one workspace, replayed one after the other, keep nothing in it between calls."""
-    c = Case(torch, [100], 128, 8192, torch.bfloat16)
-    d = Case(torch, [90], 64, 8192, torch.bfloat16, seed=1)
-    ws = torch.empty(max(moe.product_workspace("expert_product", 100, 128, 8192),
-                         moe.product_workspace("expert_product", 90, 64, 8192)), dtype=torch.uint8, device="cuda")
+    c = Case(torch, [1000], 256, 8192, torch.bfloat16)
+    d = Case(torch, [900], 192, 8192, torch.bfloat16, seed=1)
+    ws = torch.empty(max(moe.product_workspace("expert_product", 1000, 256, 8192),
+                         moe.product_workspace("expert_product", 900, 192, 8192)), dtype=torch.uint8, device="cuda")
     assert ws.numel() > 0
-    outs = [torch.empty(100, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(90, 64, dtype=torch.bfloat16, device="cuda")]
+    outs = [torch.empty(1000, 256, dtype=torch.bfloat16, device="cuda"),
+            torch.empty(900, 192, dtype=torch.bfloat16, device="cuda")]
     refs = [moe.expert_product(c.x, c.w), moe.expert_product(d.x, d.w)]
     torch.cuda.synchronize()
     graphs = []
@@ -581,13 +585,13 @@ def test_two_graphs_share_a_workspace(torch, moe):
 
 
 def test_given_buffers_and_refusals(torch, moe):
-    c = Case(torch, [100], 128, 8192, torch.bfloat16)
-    need = moe.product_workspace("expert_product", 100, 128, 8192)
+    c = Case(torch, [1000], 256, 8192, torch.bfloat16)
+    need = moe.product_workspace("expert_product", 1000, 256, 8192)
     with pytest.raises(moe.MoeError) as e:
         moe.expert_product(c.x, c.w, workspace=torch.empty(need - 256, dtype=torch.uint8, device="cuda"))
     assert e.value.status == 3
     before = torch.cuda.memory_stats()["allocation.all.allocated"]
-    out, ws = torch.empty(100, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(need, dtype=torch.uint8, device="cuda")
+    out, ws = torch.empty(1000, 256, dtype=torch.bfloat16, device="cuda"), torch.empty(need, dtype=torch.uint8, device="cuda")
     moe.expert_product(c.x, c.w, out=out, workspace=ws)
     assert torch.cuda.memory_stats()["allocation.all.allocated"] == before + 2  # the two above
     with pytest.raises(ValueError, match="w must be"):
@@ -609,13 +613,31 @@ def test_given_buffers_and_refusals(torch, moe):
     with pytest.raises(moe.MoeError):
         moe.expert_product(c.x.float(), c.w.float())
     with pytest.raises(moe.MoeError):
-        moe.expert_product(c.x[:1].expand(100, -1), c.w, workspace=ws)  # rows on top of each other
+        moe.expert_product(c.x[:1].expand(1000, -1), c.w, workspace=ws)  # rows on top of each other
     with pytest.raises(moe.MoeError):
         moe.expert_product(c.x[:, 1:9], c.w[:, :, 1:9].contiguous())    # rows off their alignment
     with pytest.raises(moe.MoeError):
         moe.int8_gated(*moe.quantize_rows(c.x), torch.zeros(1, 16, 8192, dtype=torch.int8, device="cuda"),
                        torch.zeros(1, 16, device="cuda"), dtype=torch.float32)
     torch.cuda.synchronize()
+
+
+def test_offsets_out_of_order_or_range(torch, moe):
+    """Nothing outside the matrices is touched: rows and offsets are clamped (0..100, none, 60..200 of 200 rows)."""
+    rows, n, k = 200, 72, 136
+    off = torch.tensor([-5, 100, 60, 1 << 30], dtype=torch.int32, device="cuda")
+    for scale in (1, 40):  # few rows and tiles
+        r = rows * scale
+        offsets = torch.where(off == 1 << 30, off, off * scale).to(torch.int32)
+        buf = torch.full((r + 20, n), 7.0, dtype=torch.bfloat16, device="cuda")
+        x = torch.randn(r, k, device="cuda").to(torch.bfloat16)
+        w = torch.randn(3, n, k, device="cuda").to(torch.bfloat16)
+        moe.expert_product(x, w, offsets, out=buf[10:-10])
+        assert (buf[:10] == 7.0).all() and (buf[-10:] == 7.0).all()
+        dxb = torch.full((r + 20, k), 7.0, dtype=torch.bfloat16, device="cuda")
+        _, dw = moe.expert_product_backward(buf[10:-10], x, w, offsets, dx=dxb[10:-10])
+        assert (dxb[:10] == 7.0).all() and (dxb[-10:] == 7.0).all() and not dw[1].any()
+        torch.cuda.synchronize()
 
 
 def test_no_rows(torch, moe):
@@ -670,7 +692,7 @@ def test_past_32_bits(torch, moe):
     groups, n, k = 40, 8192, 8192  # 5.4 GB of weights
     w = torch.zeros(groups, n, k, dtype=bf16, device="cuda")
     w[-1] = (torch.randn(n, k, device="cuda") / 90).to(bf16)
-    for last in (3, 100):
+    for last in (3, 100, 2000):
         x = torch.randn(last + groups - 1, k, device="cuda").to(bf16)
         off = torch.tensor(list(range(groups)) + [last + groups - 1], dtype=torch.int32, device="cuda")
         ref = x[-last:].double() @ w[-1].double().t().contiguous()

@@ -64,8 +64,8 @@ def test_workspace_holds_the_slopes_and_the_parts(lib):
     # (dg, du) of the gated backward pass
     st, n = workspace(lib, "gated_product_backward", rows=1000, n=4096, k=4096)
     assert st == 0 and n >= 1000 * 2 * 4096 * 2
-    # a few rows past the streaming kernel and a narrow result: the contraction is split
-    st, n = workspace(lib, "expert_product", rows=100, n=128, k=8192)
+    # long sums and few tiles: the contraction is split
+    st, n = workspace(lib, "expert_product", rows=1000, n=256, k=8192)
     assert st == 0 and n > 0
     # sums too short to split
     assert workspace(lib, "expert_product", rows=4096, n=8192, k=256) == (0, 0)
@@ -110,10 +110,10 @@ def test_forward_arguments_refused(lib, op):
     assert forward(lib, op, rows=4, ldout=66) == INVALID
     assert forward(lib, op, rows=4, groups=2) == INVALID         # groups without offsets
     assert forward(lib, op, rows=4, groups=2, offsets=FAKE + 2) == INVALID
-    assert forward(lib, op, rows=100, n=128, k=8192, ws_bytes=1) == SMALL
+    assert forward(lib, op, rows=1000, n=256, k=8192, ws_bytes=1) == SMALL
     assert "needs" in _lib.last_error()
-    assert forward(lib, op, rows=100, n=128, k=8192, ws=None, ws_bytes=1 << 40) == INVALID
-    assert forward(lib, op, rows=100, n=128, k=8192, ws=FAKE + 8) == INVALID
+    assert forward(lib, op, rows=1000, n=256, k=8192, ws=None, ws_bytes=1 << 40) == INVALID
+    assert forward(lib, op, rows=1000, n=256, k=8192, ws=FAKE + 8) == INVALID
     if op.startswith("int8"):
         assert forward(lib, op, rows=4, scale=None) == INVALID
         assert forward(lib, op, rows=4, w_scale=None) == INVALID
