@@ -322,13 +322,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   if constexpr (PASS == Pass::kWeightGrad) {
     // every group's tiles are spread over all XCDs: the groups' contractions
     // differ in length
-    const int tiles_m = (a.wrows + BM - 1) / BM, tiles = tiles_m * tiles_n, padded = (tiles + 7) / 8 * 8;
-    const int b = blockIdx.x;
-    const int in = JOIN ? b % tiles : xcd_unit(b % padded, tiles);
+    const int tiles_m = (a.wrows + BM - 1) / BM, tiles = tiles_m * tiles_n;
+    const int in = JOIN ? blockIdx.x : xcd_unit(blockIdx.x, tiles);
     if (in < 0) return;
-    group = (JOIN ? b / tiles : b / padded) % a.groups;
+    group = blockIdx.y;
     parts = a.splits;
-    part = JOIN ? 0 : b / (padded * a.groups);
+    part = JOIN ? 0 : blockIdx.z;
     slot = (part * a.groups + group) * tiles + in;
     slot_step = a.groups * tiles;
     const int band = in / (kBand * tiles_n), high = min(kBand, tiles_m - band * kBand);
@@ -354,18 +353,22 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
     if (a.groups > 1) __syncthreads();  // the lookup's LDS is free
   }
   const int stages = (klen + BK - 1) / BK;
-  const int st0 = (int)((int64_t)stages * part / parts), st1 = (int)((int64_t)stages * (part + 1) / parts);
+  // (at most 2^16 stages and 8 parts; short contractions feel a division)
+  const int st0 = parts == 1 ? 0 : stages * part / parts, st1 = parts == 1 ? stages : stages * (part + 1) / parts;
   // raw sums of a part: every lane's, 16 bytes each
   auto raw = [&](int at, int i, int j) {
     return reinterpret_cast<acc_t*>(a.partial + (int64_t)at * (BM * BN * 4)) + ((wave * MI + i) * NJ + j) * 64 + lane;
   };
 
   acc_t acc[MI][NJ];
+  auto clear = [&]() {
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[i][j] = acc_t{};
+      for (int j = 0; j < NJ; ++j) acc[i][j] = acc_t{};
+  };
   if constexpr (JOIN) {
+    clear();
     for (int s = 0; s < parts; ++s)
 #pragma unroll
       for (int i = 0; i < MI; ++i)
@@ -487,6 +490,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
     begin_q(st0 + 1);
 #pragma unroll
     for (int c = 0; c < QI; ++c) copy_q(3, c);
+    __builtin_amdgcn_sched_barrier(0);
+    clear();  // while the first copies are under way
     wait_copies<PI + QI>();
     lds_only_barrier();
     // Iteration i: ps and qs hold stage i, pn and qn stage i + 1, `spare` is
@@ -558,6 +563,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
       }
     }
     wait_copies<0>();  // the zeros of stages past the end
+  } else {
+    clear();
   }
   if (parts > 1) {
 #pragma unroll
@@ -665,15 +672,15 @@ void launch_tile(const ProductArgs& a, hipStream_t s) {
   const int no = RES == Result::kGated ? BN / 2 : BN;
   const int tiles_n = ((RES == Result::kGated ? a.cols / 2 : a.cols) + no - 1) / no;
   const int threads = 64 * WM * WN;
-  int blocks, joins;
+  dim3 blocks, joins;
   if (PASS == Pass::kWeightGrad) {
     const int tiles = (a.wrows + BM - 1) / BM * tiles_n;
-    blocks = a.splits * a.groups * ((tiles + 7) / 8 * 8);  // xcd_unit deals units in rounds of 8
-    joins = a.groups * tiles;
+    blocks = dim3((tiles + 7) / 8 * 8, a.groups, a.splits);  // xcd_unit deals units in rounds of 8
+    joins = dim3(tiles, a.groups);
   } else {
     const int tiles = row_tile_bound(a.rows, a.groups, BM) * tiles_n;
-    blocks = (tiles + 7) / 8 * 8 + (a.splits > 1 ? split_units(BM, tiles, a.splits) + 8 : 0);
-    joins = std::min(tiles, (BM == 256 ? 256 : 512) / 2);  // a split tile has at least two parts
+    blocks = dim3((tiles + 7) / 8 * 8 + (a.splits > 1 ? split_units(BM, tiles, a.splits) + 8 : 0));
+    joins = dim3(std::min(tiles, (BM == 256 ? 256 : 512) / 2));  // a split tile has at least two parts
   }
   product_tile_kernel<T, PASS, RES, false, BM, BN, WM, WN><<<blocks, threads, 0, s>>>(a);
   if (a.splits > 1) product_tile_kernel<T, PASS, RES, true, BM, BN, WM, WN><<<joins, threads, 0, s>>>(a);
