@@ -23,16 +23,26 @@ from . import _lib
 ACTIVATIONS = {"silu": _lib.MOE_ACT_SILU, "gelu": _lib.MOE_ACT_GELU}
 
 
-@lru_cache(maxsize=None)
-def _torch():
-    import torch
-    return torch
+class _Torch:
+    """What the calls need of torch, looked up once (a small product is bound by
+    the host, where each of these lookups would show)."""
+
+    def __init__(self):
+        import torch
+        self.torch = torch
+        self.int8, self.float32, self.int32, self.bfloat16 = torch.int8, torch.float32, torch.int32, torch.bfloat16
+        self.types = {torch.bfloat16: _lib.MOE_TYPE_BF16, torch.float16: _lib.MOE_TYPE_FP16,
+                      torch.float32: _lib.MOE_TYPE_FP32}
+        self.current_device = torch.cuda.current_device
+        # the raw handle without a Stream object around it (2 us less), where this torch has it
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda index: torch.cuda.current_stream(index).cuda_stream)
+        self.lib = _lib.load()
 
 
 @lru_cache(maxsize=None)
-def _types():
-    torch = _torch()
-    return {torch.bfloat16: _lib.MOE_TYPE_BF16, torch.float16: _lib.MOE_TYPE_FP16, torch.float32: _lib.MOE_TYPE_FP32}
+def _env():
+    return _Torch()
 
 
 @lru_cache(maxsize=1024)
@@ -50,11 +60,11 @@ def product_workspace(op: str, rows: int, n: int, k: int, groups: int = 1, dtype
     if op not in _lib.MOE_OPS:
         raise ValueError(f"op must be one of {sorted(_lib.MOE_OPS)}, not {op!r}")
     return _shape(_lib.MOE_OPS[op], int(rows), int(n), int(k), int(groups),
-                  _type(dtype or _torch().bfloat16), _act(activation) if "gated" in op else 0)[1]
+                  _type(dtype or _env().bfloat16), _act(activation) if "gated" in op else 0)[1]
 
 
 def _type(dtype) -> int:
-    t = _types().get(dtype)
+    t = _env().types.get(dtype)
     if t is None:
         raise ValueError(f"unsupported dtype {dtype}")
     return t
@@ -73,24 +83,24 @@ class _Call:
     enqueues.  (Short calls are bound by the host: the checks are ordered so
     that what is right costs one comparison each.)"""
 
-    __slots__ = ("lib", "index", "device", "guards", "stream")
+    __slots__ = ("env", "lib", "index", "device", "guards", "stream", "like")
 
     def __init__(self, first, stream):
-        cuda = _torch().cuda
-        self.lib = _lib.load()
-        self.index = first.get_device()
-        if self.index < 0:
+        env = self.env = _env()
+        self.lib = env.lib
+        self.like = first
+        index = self.index = first.get_device()
+        if index < 0:
             raise ValueError("the tensors must be on a GPU")
-        self.device = first.device
         self.guards = ()
-        if cuda.current_device() != self.index:
-            self.guards = (cuda.device(self.index),)
+        if env.current_device() != index:
+            self.guards = (env.torch.cuda.device(index),)
         if stream is None:
-            self.stream = cuda.current_stream(self.index).cuda_stream
+            self.stream = env.raw_stream(index)
         else:
-            if stream.device != self.device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
-            self.guards += (cuda.stream(stream),)
+            if stream.device != first.device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
+            self.guards += (env.torch.cuda.stream(stream),)
             self.stream = stream.cuda_stream
 
     def __enter__(self):
@@ -101,6 +111,9 @@ class _Call:
     def __exit__(self, *exc):
         for g in reversed(self.guards):
             g.__exit__(*exc)
+
+    def empty(self, shape, dtype):
+        return self.like.new_empty(shape, dtype=dtype)
 
     def rows(self, name, t, rows, width, dtype):
         """(pointer, row stride) of a [rows, width] matrix."""
@@ -120,8 +133,8 @@ class _Call:
         return t.data_ptr()
 
     def refuse(self, name, t, shape, dtype):
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, not on {self.device}")
+        if t.get_device() != self.index:
+            raise ValueError(f"{name} is on {t.device}, not on {self.like.device}")
         if t.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
@@ -129,24 +142,24 @@ class _Call:
     def offsets(self, offsets, groups):
         if offsets is None:
             return None
-        return self.plain("offsets", offsets, (groups + 1,), _torch().int32)
+        return self.plain("offsets", offsets, (groups + 1,), self.env.int32)
 
     def workspace(self, workspace, need):
         """(pointer, bytes, tensor kept alive until the call returns)."""
         if workspace is None:
             if need == 0:
                 return None, 0, None
-            workspace = _torch().empty(need, dtype=_torch().uint8, device=self.device)
+            workspace = self.empty(need, self.env.torch.uint8)
         else:
             if workspace.get_device() != self.index:
-                raise ValueError(f"workspace is on {workspace.device}, not on {self.device}")
+                raise ValueError(f"workspace is on {workspace.device}, not on {self.like.device}")
             if not workspace.is_contiguous():
                 raise ValueError("workspace must be contiguous")
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
     def result(self, name, out, rows, width, dtype):
         if out is None:
-            out = _torch().empty((rows, width), dtype=dtype, device=self.device)
+            out = self.empty((rows, width), dtype)
             return out, out.data_ptr(), width
         return (out, *self.rows(name, out, rows, width, dtype))
 
@@ -171,31 +184,29 @@ def _matrix_rows(name, t):
 def quantize_rows(x, codes=None, scale=None, stream=None):
     """(codes int8 [rows, k], scale fp32 [rows]) of x [rows, k] (bf16 or fp16):
     scale = max|row| / 127, codes = rint(row / scale) (moe_quantize_rows)."""
-    torch = _torch()
     rows = _matrix_rows("x", x)
     k = x.shape[1]
     with _Call(x, stream) as c:
         px, ldx = c.rows("x", x, rows, k, x.dtype)
-        codes, pc, ldc = c.result("codes", codes, rows, k, torch.int8)
+        codes, pc, ldc = c.result("codes", codes, rows, k, c.env.int8)
         if scale is None:
-            scale = torch.empty(rows, dtype=torch.float32, device=c.device)
-        ps = c.plain("scale", scale, (rows,), torch.float32)
+            scale = c.empty(rows, c.env.float32)
+        ps = c.plain("scale", scale, (rows,), c.env.float32)
         _lib.check(c.lib.moe_quantize_rows(rows, k, _type(x.dtype), px, ldx, pc, ldc, ps, c.stream))
     return codes, scale
 
 
 def _int8(op, codes, scale, w, w_scale, offsets, activation, out, dtype, workspace, stream):
-    torch = _torch()
     gated = activation is not None
     rows = _matrix_rows("codes", codes)
     groups, n, k = _weights(w, gated)
     if dtype is None:
-        dtype = out.dtype if out is not None else torch.bfloat16
+        dtype = out.dtype if out is not None else _env().bfloat16
     with _Call(codes, stream) as c:
-        pc, ldc = c.rows("codes", codes, rows, k, torch.int8)
-        ps = c.plain("scale", scale, (rows,), torch.float32)
-        pw = c.plain("w", w, w.shape, torch.int8)
-        pws = c.plain("w_scale", w_scale, w.shape[:-1], torch.float32)
+        pc, ldc = c.rows("codes", codes, rows, k, c.env.int8)
+        ps = c.plain("scale", scale, (rows,), c.env.float32)
+        pw = c.plain("w", w, w.shape, c.env.int8)
+        pws = c.plain("w_scale", w_scale, w.shape[:-1], c.env.float32)
         po = c.offsets(offsets, groups)
         shape, need = _shape(op, rows, n, k, groups, _type(dtype), _act(activation) if gated else 0)
         out, pout, ldout = c.result("out", out, rows, n, dtype)
@@ -257,7 +268,6 @@ def gated_product(x, w, offsets=None, activation="silu", save=False, out=None, g
 
 
 def _backward(name, dy, gate_up, x, w, offsets, activation, need_dx, need_dw, dx, dw, dw_dtype, workspace, stream):
-    torch = _torch()
     gated = activation is not None
     rows = _matrix_rows("dh" if gated else "dy", dy)
     groups, n, k = _weights(w, gated)
@@ -274,7 +284,7 @@ def _backward(name, dy, gate_up, x, w, offsets, activation, need_dx, need_dw, dx
             dx, pdx, lddx = c.result("dx", dx, rows, k, dtype)
         if need_dw:
             if dw is None:
-                dw = torch.empty(w.shape, dtype=dw_dtype or dtype, device=c.device)
+                dw = c.empty(w.shape, dw_dtype or dtype)
             pdw = c.plain("dw", dw, w.shape, dw_dtype or dw.dtype)
         ws, ws_bytes, _alive = c.workspace(workspace, need)
         dw_type = _type(dw.dtype) if need_dw else shape.type
