@@ -259,29 +259,52 @@ __device__ __forceinline__ bool find_row_tile(const ProductArgs& a, int tiles_n,
 
 // ---- LDS-tiled product ------------------------------------------------------
 // A block computes BM x BN of a group's product on WM x WN waves, each wave a
-// grid of 32 x 32 matrix-core tiles.  The contraction is walked in stages of
-// 128 bytes a row (64 16-bit values, 128 codes) through two LDS buffers filled
-// by direct global -> LDS copies.  An operand comes in one of two layouts:
+// grid of 16 x 16 matrix-core tiles.  The contraction is walked in stages of
+// 128 bytes a row (64 16-bit values, 128 codes).  One operand's stage is a slot
+// of a ring of kRing LDS buffers that direct global -> LDS copies fill: the
+// current stage, the next one, and the one after for P.  An operand comes in
+// one of two layouts:
 //  - contraction contiguous in memory (x, codes, w in the forward product):
 //    LDS rows of 128 bytes, 16-byte chunks swizzled by the row so that the 16
 //    rows of one read cycle fall on different banks;
 //  - contraction across the rows (w in the input gradient; dy and x in the
 //    weight gradient): LDS holds 64 rows of BM (or BN) values and the
 //    transposing LDS read hands each lane 4 consecutive contraction values of
-//    its column; chunks are swizzled by row % 4, the 4 rows that one read
-//    cycle covers.  No operand is ever transposed in memory.
-// In the last of a stage's four steps the block waits for the next stage's
-// copies, refills the buffer just read and reads the next stage's first
-// fragments before the step's products, which hide the LDS latency behind the
-// barrier.  Missing rows, columns and the contraction's tail are zeros (out of
-// range buffer loads), so they add nothing to the sums.
+//    its column; chunks are swizzled by row, so that the 8 rows that one read
+//    cycle covers fall on different banks.  No operand is ever transposed in
+//    memory.
+// Missing rows, columns, the contraction's tail and stages past the end are
+// zeros (out of range buffer loads), so they add nothing to the sums.
 //
 // The matrix cores take Q's values as A and P's as B: a lane then holds four
 // consecutive columns of one result row.  16-bit results go through LDS and
 // leave as whole rows of 16-byte stores; fp32 ones leave from registers.
 //
 // Gated: the block's columns are BN/2 gate and the same BN/2 up columns,
-// interleaved by 32 so that a wave holds g and u of the same elements.
+// interleaved by 16 so that a wave holds g and u of the same elements.
+//
+// What bounds it: power.  At 8192^3 in bf16 (random values) the chip holds
+// 1.85 GHz with the matrix cores busy 78% of the cycles: 1500 TFLOP/s forward,
+// 1480 input gradient, 1460 weight gradient (a large library product on the
+// same card: 1570, 86% at 1.77 GHz), codes 2800 TOP/s (library: 2390).  What it
+// took, each step timed at that size (forward / weight gradient / codes, us):
+//  - 32 x 32 tiles, two buffers of both operands, all copies issued after the
+//    barrier: 854 / 941 / 462.  A compute unit accepts a 1 KB copy every 16
+//    cycles, so eight waves that issue eight each wait for each other with the
+//    matrix cores idle; a deeper ring of half stages did not help (884);
+//  - copies and fragment reads spread between the products: 824 / 790 / 438;
+//  - 16 x 16 tiles: 777 / 749 / 401.  In a loop of products alone they run
+//    at 2010 TFLOP/s, 32 x 32 ones at 1800: less power per product;
+//  - products at raised wave priority, and the hand-over to the next stage
+//    three eighths into its second step: 750 / 763 / 397.
+// Four waves of 128 x 128 (fewer LDS reads, one wave per SIMD) spilled and lost
+// a third.  128 x 128 blocks, two per compute unit, reach 1180 TFLOP/s (half
+// the products per byte copied) and serve where few 256-wide ones would run.
+// A tile costs about 8 us beside its stages (start 1.5, first copies 1.3, the
+// results' way through LDS 1.8 and out 3), as much as 5 of them.  One block
+// per compute unit that takes tiles from a queue and copies the next tile's
+// first stages under the results' writing was no faster (its bookkeeping took
+// registers from the loop).
 //
 // JOIN: the block adds the raw sums of a split tile's parts, in order, instead
 // of computing them, and writes the result.

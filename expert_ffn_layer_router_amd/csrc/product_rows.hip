@@ -17,7 +17,9 @@ __device__ __forceinline__ uint32_t max_lanes(uint32_t v) {
 // ---- quantise rows ------------------------------------------------------------
 // WPR waves share a row; each thread keeps CH chunks of 8 values in registers,
 // so the row is read once (longer rows read what does not fit a second time,
-// from the caches).  Bound by memory: 3 bytes per value.
+// from the caches).  Bound by memory, 3 bytes per value: 8192 rows of 14336 in
+// 66 us, 5.3 TB/s (a large copy reaches 4.8); 16 rows of 4096 in 3.1 us, which
+// is a launch and two trips to memory.
 //
 // The code is the exact quotient 127 x / a rounded to nearest even.  With the
 // row scaled by a power of two so that a is in [1/2, 1) (no overflow or
@@ -97,7 +99,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(int rows, int k, bool fp1
 
 // ---- slopes of the gated block ------------------------------------------------
 // dg = dh u act'(g), du = dh act(g); 8 columns per thread.  Bound by memory:
-// 10 bytes per element of dh.
+// 10 bytes per element of dh (4096 rows of 14336: 93-117 us, 5.0-6.3 TB/s).
 __global__ __launch_bounds__(256) void gated_slopes_kernel(int rows, int n, bool fp16, int act,
                                                            const uint16_t* __restrict__ dh, int64_t lddh,
                                                            const uint16_t* __restrict__ gu, int64_t ldgu,

@@ -10,6 +10,14 @@
 // kilobytes of each row in turn.  The rows come from the caches in the same
 // fragment layout.  The waves' sums meet in LDS and are added in wave order, so
 // the result does not depend on timing.
+//
+// 32 rows over 8 groups of 14336 gated columns of 4096 codes: 158 us, 5.9 TB/s
+// (a read-only stream reaches 6.7); 16 rows x one group of 6400 gated columns
+// of 4096 in bf16: 25 us, 4.2 TB/s: 400 blocks, whose start and end show.
+// Eight waves dealt runs of four steps in turn took 221 us for the first:
+// what counts is how many consecutive bytes of a row a wave asks for.  The
+// non-temporal hint, which drops a line's second half before it is asked for,
+// cost 15%.
 #include <type_traits>
 
 #include "product_core.h"
