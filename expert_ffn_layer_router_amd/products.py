@@ -11,7 +11,10 @@ a result that the call allocates: unspecified).
 Row matrices may have any row stride that is a multiple of 8 elements (16 for
 codes); weights, scales and offsets are contiguous.  A call runs on `stream`
 (default: the current stream of the tensors' device) and allocates what it is
-not given there; with `out` and `workspace` given it allocates nothing."""
+not given there; with `out` and `workspace` given it allocates nothing.  On
+another stream than the current one the caller orders the call after what
+wrote its inputs; their memory is kept from reuse until it is done.  Nothing is
+recorded for autograd: the backward calls are the caller's."""
 
 from __future__ import annotations
 
@@ -83,7 +86,7 @@ class _Call:
     enqueues.  (Short calls are bound by the host: the checks are ordered so
     that what is right costs one comparison each.)"""
 
-    __slots__ = ("env", "lib", "index", "device", "guards", "stream", "like")
+    __slots__ = ("env", "lib", "index", "guards", "stream", "like", "other")
 
     def __init__(self, first, stream):
         env = self.env = _env()
@@ -95,6 +98,7 @@ class _Call:
         self.guards = ()
         if env.current_device() != index:
             self.guards = (env.torch.cuda.device(index),)
+        self.other = None
         if stream is None:
             self.stream = env.raw_stream(index)
         else:
@@ -102,6 +106,8 @@ class _Call:
                 raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
             self.guards += (env.torch.cuda.stream(stream),)
             self.stream = stream.cuda_stream
+            if self.stream != env.raw_stream(index):
+                self.other = stream
 
     def __enter__(self):
         for g in self.guards:
@@ -122,6 +128,8 @@ class _Call:
         stride, one = t.stride()
         if one != 1:
             raise ValueError(f"the values of a row of {name} must be contiguous")
+        if self.other is not None:
+            t.record_stream(self.other)
         return t.data_ptr(), (stride if rows > 1 else width)
 
     def plain(self, name, t, shape, dtype):
@@ -130,6 +138,8 @@ class _Call:
             self.refuse(name, t, shape, dtype)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+        if self.other is not None:
+            t.record_stream(self.other)
         return t.data_ptr()
 
     def refuse(self, name, t, shape, dtype):
@@ -155,6 +165,8 @@ class _Call:
                 raise ValueError(f"workspace is on {workspace.device}, not on {self.like.device}")
             if not workspace.is_contiguous():
                 raise ValueError("workspace must be contiguous")
+            if self.other is not None:
+                workspace.record_stream(self.other)
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
     def result(self, name, out, rows, width, dtype):

@@ -537,6 +537,23 @@ def test_same_call_same_bits_on_any_stream(torch, moe, rows):
             assert torch.equal(a, b) and torch.equal(a, c), name
 
 
+def test_inputs_freed_while_another_stream_reads_them(torch, moe):
+    """Inputs dropped right after a call on a side stream keep their memory until it is done."""
+    side = torch.cuda.Stream()
+    w = torch.randn(1, 4096, 4096, device="cuda").to(torch.bfloat16)
+    for _ in range(4):
+        x = torch.randn(8192, 4096, device="cuda").to(torch.bfloat16)
+        ref = moe.expert_product(x, w)
+        torch.cuda.synchronize()
+        moe.expert_product(x, w, stream=side)  # keeps the side stream busy first
+        y = moe.expert_product(x, w, stream=side)
+        where = x.data_ptr()
+        del x
+        other = [torch.full((8192, 4096), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        torch.cuda.synchronize()
+        assert torch.equal(y, ref), [t.data_ptr() == where for t in other]
+
+
 @pytest.mark.parametrize("rows", [7, 300, 2500])
 def test_captured_calls_replay(torch, moe, rows):
     """Each call captured into a graph with its buffers; replays follow rewritten inputs, with eager work between."""
