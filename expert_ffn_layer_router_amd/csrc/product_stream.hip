@@ -185,15 +185,17 @@ void launch_mt(const ProductArgs& a, hipStream_t s) {
 }
 
 // A block of 32 columns reads the rows half as often, one of 16 makes twice as
-// many blocks: 96 rows over 64 groups of 4096 columns of 2048 (8192 blocks of
-// 32): 92 against 106 us; 16 rows x one group of 4096 columns of 14336 (128
-// blocks): 45 against 34 us; 1024 blocks: within 2%.
-constexpr int kWideBlocks = 2048;
+// many blocks.  With more than 4 rows a group and blocks for most compute units
+// the wide ones win: 16 rows x 12800 columns of 4096 in bf16: 29.6 against 35.3
+// us; 256 rows over 16 groups of 4096 columns of 2048: 58 against 71; 16 x 6400
+// (200 blocks of 32): 18.2 against 19.8.  16 x 4096 of 14336 (128 blocks): 45
+// against 34; 96 rows over 64 groups, codes: 58 against 51.
+constexpr int kWideBlocks = 192, kWideRows = 4;
 template <Num T, Result RES>
 void launch_stream(const ProductArgs& a, hipStream_t s) {
   if constexpr (RES == Result::kGated)
     launch_mt<T, RES, 2>(a, s);
-  else if ((int64_t)a.groups * ((a.cols + 31) / 32) >= kWideBlocks)
+  else if ((int64_t)a.groups * ((a.cols + 31) / 32) >= kWideBlocks && a.rows > kWideRows * a.groups)
     launch_mt<T, RES, 2>(a, s);
   else
     launch_mt<T, RES, 1>(a, s);
