@@ -18,21 +18,28 @@ constexpr int64_t kMaxStride = 1 << 20;
 // The streaming kernel takes calls with up to 16 rows per group on average:
 // reading the used groups' weights is then most of the time, and it reads them
 // faster than the tiles do, whose rows are mostly padding (16 rows x one group
-// of 6400 gated columns of 4096 in bf16: 29.6 against 38.4 us; 256 rows over
-// 16 groups of 2048: 106 against 166; 384 over 64: 376 against 562; uneven
-// groups cost it: 128 rows over 16 groups of 4096 columns of 6400, 47 in the
-// largest: 194 against 158).
+// of 6400 gated columns of 4096 in bf16: 25.8 against 38.4 us; 256 rows over
+// 16 groups of 4096 columns of 2048: 55 against 75; 384 over 64 of 2048 gated
+// columns of 4096: 374 against 565; uneven groups cost it: 128 rows over 16
+// groups of 4096 columns of 6400, 47 in the largest: 169 against 158).
 constexpr int kStreamGroupRows = 16;
-// With more rows its blocks read them over and over (and the weights once for
-// every 64 rows of a group), which still beats the tiles' fixed costs, a
-// second kernel for the split contraction among them, while it is little and
-// the groups and rows are not long enough to fill the chip with tiles: 64 rows
-// x 4096 columns of 2048 codes: 8.9 against 16.1 us; 100 rows x 2048 gated
-// columns of 2048 in bf16: 15.8 against 22.1; 256 x 1024 of 2048: 13.2 against
-// 20.6; 64 x the 6400 columns (210 MB of rows): 53 against 38; 300 x 128 of
-// 8192: 39 against 23; 2048 x 512 of 512: 13.6 against 10.1.
-constexpr int64_t kStreamExtraBytes = 48 << 20;
-constexpr int kStreamExtraRows = 512, kStreamExtraRowBytes = 8192;
+// With more rows its blocks read them again for every 32 columns, and the
+// weights again for every 64 rows of a group.  That still beats the tiles'
+// fixed costs, a second kernel for the split contraction among them, as long
+// as these reads are few, in bytes (what the caches deliver) and in 64-byte
+// steps' worth of rows (short rows: what a block's start and end cost).
+// Below the limits, in bf16: 256 rows x 2048 columns of 2048 (89 MB, 22 k
+// rows): 11.2 against 23.0 us; 128 x 4096 of 4096 (161 MB): 17.7 against 23.5;
+// 1000 x 512 of 4096 (193 MB): 18.8 against 24.6; 2000 x 512 of 512 (49 MB,
+// 49 k rows): 9.0 against 9.9; 40 x 25600 of 1024 (31 k rows): 22.6 against
+// 20.0.  Above: 64 x 12800 of 4096 (201 MB): 44.8 against 39.9; 300 x 4096 of
+// 1024 (54 k rows): 15.4 against 13.8; 512 x 8192 of 192 (185 k): 14.4 against
+// 8.6; 1536 rows over 64 groups of 4096 columns of 2048 (774 MB): 281 against
+// 218.  The rows of one of many uneven groups are few blocks' work: 1000 rows
+// over 16 groups of 1024 columns of 1024, 202 in the largest: 18.4 against
+// 15.2; 800 over 8 of 2048: 22.7 against 24.8.
+constexpr int64_t kStreamExtraBytes = 196 << 20, kStreamExtraRows = 48 << 10;
+constexpr int kStreamExtraGroups = 8;
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -44,11 +51,11 @@ ProductPlan plan_product(Num num, Pass pass, Result res, const ProductArgs& a) {
   const bool gated = res == Result::kGated, wg = pass == Pass::kWeightGrad;
   if (pass == Pass::kForward) {
     const int64_t row_bytes = (int64_t)a.contract * (num == Num::kInt8 ? 1 : 2);
-    const int64_t row_reads = (int64_t)(a.cols / (gated ? 32 : 16) + 1) * a.rows * row_bytes;
-    const int64_t weight_reads = (a.rows - 1) / (64 * a.groups) * ((int64_t)a.groups * a.cols * row_bytes);
+    const int64_t row_reads = (int64_t)(a.cols / 32 + 1) * a.rows;
+    const int64_t weight_reads = (a.rows - 1) / (64 * a.groups) * ((int64_t)a.groups * a.cols);
+    const int64_t extra = row_reads + weight_reads;  // rows of either operand
     if (a.rows <= kStreamGroupRows * a.groups ||
-        (a.rows <= kStreamExtraRows * a.groups && row_bytes <= kStreamExtraRowBytes &&
-         (row_reads + weight_reads) / 2 <= kStreamExtraBytes)) {
+        (a.groups <= kStreamExtraGroups && extra <= kStreamExtraRows && extra * row_bytes <= kStreamExtraBytes)) {
       p.family = Family::kStream;
       return p;
     }

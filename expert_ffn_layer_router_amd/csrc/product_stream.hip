@@ -44,137 +44,174 @@ __global__ __launch_bounds__(64 * kStreamWaves, MT == 4 ? 2 : 4) void product_st
   int begin, end;
   group_rows(a.offsets, a.rows, group, begin, end);
   begin = __builtin_amdgcn_readfirstlane(begin) + blockIdx.z * 16 * MT;
-  const int live = min(16 * MT, __builtin_amdgcn_readfirstlane(end) - begin);
-  if (live <= 0) return;
+  end = __builtin_amdgcn_readfirstlane(end);
+  if (begin >= end) return;
   const int F = a.cols / 2, ncols = GATED ? F : a.cols;
   const int n0 = blockIdx.x * NO;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, quad = lane >> 4;
 
+  // lane l loads 16 bytes of row l / 4 of a tile, so that four neighbours ask
+  // for 64 bytes in a row, and multiplies those of row l % 16
+  const int lrow = lane >> 2, lbyte = 16 * (lane & 3);
+  const int from = 4 * (4 * l16 + quad);  // the lane that loaded them, in bytes
   const char* wbase = a.q + (int64_t)group * a.q_group + (int64_t)n0 * a.ldq;
   __amdgpu_buffer_rsrc_t wr[NC];
   uint32_t wv[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     wr[c] = buffer_at(GATED ? wbase + (c ? (int64_t)F * a.ldq : 0) : wbase);
-    const int r = (GATED ? 0 : 16 * c) + l16;
-    wv[c] = n0 + r < ncols ? (uint32_t)(r * a.ldq + 16 * quad) : kNoLoad;
+    const int r = (GATED ? 0 : 16 * c) + lrow;
+    wv[c] = n0 + r < ncols ? (uint32_t)(r * a.ldq + lbyte) : kNoLoad;
   }
-  const __amdgpu_buffer_rsrc_t xr = buffer_at(a.p + (int64_t)begin * a.ldp);
-  uint32_t xv[MT];
+  // the group's row tiles: this block's and every gridDim.z-th after it (the
+  // grid has one for every tile with MT < 4, whose registers are full)
+  for (bool first = true; first || (MT == 4 && begin < end); begin += gridDim.z * 16 * MT, first = false) {
+    const int live = min(16 * MT, end - begin);
+    if (!first) __syncthreads();  // the last tile's sums have been read
+    const __amdgpu_buffer_rsrc_t xr = buffer_at(a.p + (int64_t)begin * a.ldp);
+    uint32_t xv[MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) xv[m] = 16 * m + l16 < live ? (uint32_t)((16 * m + l16) * a.ldp + 16 * quad) : kNoLoad;
+    for (int m = 0; m < MT; ++m) xv[m] = 16 * m + lrow < live ? (uint32_t)((16 * m + lrow) * a.ldp + lbyte) : kNoLoad;
 
-  acc_t acc[MT][NC];
+    acc_t acc[MT][NC];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int c = 0; c < NC; ++c) acc[m][c] = acc_t{};
+      for (int c = 0; c < NC; ++c) acc[m][c] = acc_t{};
 
-  const int bytes = a.contract * ES;  // of a row
-  const int steps = (bytes + 63) / 64;
-  // the row tiles in use are a compile-time count, so that the loop holds no branches
-  auto body = [&](auto tag) {
-    constexpr int ML = decltype(tag)::value;
-    constexpr int kRun = ML == 1 ? 4 : 2;  // steps loaded together, as the registers allow
-    // this wave's steps [s, s1): contiguous, so that a wave reads long runs of
-    // each row
-    const int s1 = (int)((int64_t)steps * (wave + 1) / kStreamWaves);
-    int s = (int)((int64_t)steps * wave / kStreamWaves);
-    u32x4 w[2][kRun][NC], x[2][kRun][ML];
-    auto load = [&](int b, int at) {
+    const int bytes = a.contract * ES;  // of a row
+    const int steps = (bytes + 63) / 64;
+    // the row tiles in use are a compile-time count, so that the loop holds no branches
+    auto body = [&](auto tag) {
+      constexpr int ML = decltype(tag)::value;
+      constexpr int kRun = ML == 1 && NC == 1 ? 4 : 2;  // steps loaded together, as the registers allow
+      // this wave's steps [s, s1): contiguous, so that a wave reads long runs of
+      // each row
+      const int s1 = (int)((int64_t)steps * (wave + 1) / kStreamWaves);
+      int s = (int)((int64_t)steps * wave / kStreamWaves);
+      u32x4 w[2][kRun][NC], x[2][kRun][ML];
+      auto load = [&](int b, int at) {
 #pragma unroll
-      for (int u = 0; u < kRun; ++u) {
-        const bool in = (at + u) * 64 + 16 * quad < bytes && at + u < s1;  // bytes: a multiple of 16
+        for (int u = 0; u < kRun; ++u) {
+          const bool in = (at + u) * 64 + lbyte < bytes && at + u < s1;  // bytes: a multiple of 16
 #pragma unroll
-        for (int c = 0; c < NC; ++c) w[b][u][c] = load16(wr[c], in ? wv[c] : kNoLoad, (uint32_t)(at + u) * 64);
+          for (int c = 0; c < NC; ++c) w[b][u][c] = load16(wr[c], in ? wv[c] : kNoLoad, (uint32_t)(at + u) * 64);
 #pragma unroll
-        for (int m = 0; m < ML; ++m) x[b][u][m] = load16(xr, in ? xv[m] : kNoLoad, (uint32_t)(at + u) * 64);
-      }
-    };
-    auto multiply = [&](int b) {
-#pragma unroll
-      for (int u = 0; u < kRun; ++u)
-#pragma unroll
-        for (int m = 0; m < ML; ++m)
-#pragma unroll
-          for (int c = 0; c < NC; ++c) acc[m][c] = mfma16x16<T>(w[b][u][c], x[b][u][m], acc[m][c]);
-    };
-    if (s < s1) load(0, s);
-    while (s < s1) {
-      if (s + kRun < s1) load(1, s + kRun);
-      multiply(0);
-      s += kRun;
-      if (s >= s1) break;
-      if (s + kRun < s1) load(0, s + kRun);
-      multiply(1);
-      s += kRun;
-    }
-  };
-  const int tiles = (live + 15) / 16;
-  if (MT == 1 || tiles == 1)
-    body(std::integral_constant<int, 1>{});
-  else if (MT == 2 || tiles == 2)
-    body(std::integral_constant<int, MT < 2 ? 1 : 2>{});
-  else
-    body(std::integral_constant<int, MT>{});
-
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int c = 0; c < NC; ++c) part[wave][m * NC + c][lane] = acc[m][c];
-  __syncthreads();
-
-  // lane l of tile (m, c): row 16m + l % 16, columns 16c + 4 (l / 16) ..
-  const bool fp16 = T == Num::kFp16 || (T == Num::kInt8 && a.out_type == MOE_TYPE_FP16);
-  constexpr int kTiles = GATED ? MT : MT * NC;  // result tiles
-  for (int tile = wave; tile < kTiles; tile += kStreamWaves) {
-    const int m = GATED ? tile : tile / NC, c = GATED ? 0 : tile % NC;
-    const int row = 16 * m + l16, col = n0 + 16 * c + 4 * quad;
-    if (row >= live || col >= ncols) continue;
-    auto total = [&](int t, int up) -> f32x4 {
-      acc_t v = part[0][t][lane];
-#pragma unroll
-      for (int w = 1; w < kStreamWaves; ++w) v += part[w][t][lane];
-      f32x4 f;
-      if constexpr (T == Num::kInt8) {
-        const float ps = a.pscale[begin + row];
-        const f32x4 s = *reinterpret_cast<const f32x4*>(a.qscale + (int64_t)group * a.cols + (up ? F : 0) + col);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = (float)v[e] * ps * s[e];
-      } else {
-        f = v;
-      }
-      return f;
-    };
-    f32x4 v = total(GATED ? m * NC : tile, 0);
-    if constexpr (RES == Result::kWide) {
-      *reinterpret_cast<f32x4*>((float*)a.out + (int64_t)(begin + row) * a.ldout + col) = v;
-    } else {
-      if constexpr (GATED) {
-        const f32x4 u = total(m * NC + 1, 1);
-        if (T != Num::kInt8 && a.keep) {
-          uint16_t* k = a.keep + (int64_t)(begin + row) * a.ldkeep + col;
-          *reinterpret_cast<u32x2*>(k) = u32x2{pack_half(fp16, v[0], v[1]), pack_half(fp16, v[2], v[3])};
-          *reinterpret_cast<u32x2*>(k + F) = u32x2{pack_half(fp16, u[0], u[1]), pack_half(fp16, u[2], u[3])};
+          for (int m = 0; m < ML; ++m) x[b][u][m] = load16(xr, in ? xv[m] : kNoLoad, (uint32_t)(at + u) * 64);
         }
+      };
+      auto fragment = [&](u32x4 v) {
+        u32x4 f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = activate(a.act, v[e]) * u[e];
+        for (int e = 0; e < 4; ++e) f[e] = __builtin_amdgcn_ds_bpermute(from, v[e]);
+        return f;
+      };
+      auto multiply = [&](int b) {
+#pragma unroll
+        for (int u = 0; u < kRun; ++u) {
+          u32x4 wf[NC];
+#pragma unroll
+          for (int c = 0; c < NC; ++c) wf[c] = fragment(w[b][u][c]);
+#pragma unroll
+          for (int m = 0; m < ML; ++m) {
+            const u32x4 xf = fragment(x[b][u][m]);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) acc[m][c] = mfma16x16<T>(wf[c], xf, acc[m][c]);
+          }
+        }
+      };
+      if (s < s1) load(0, s);
+      while (s < s1) {
+        if (s + kRun < s1) load(1, s + kRun);
+        multiply(0);
+        s += kRun;
+        if (s >= s1) break;
+        if (s + kRun < s1) load(0, s + kRun);
+        multiply(1);
+        s += kRun;
       }
-      *reinterpret_cast<u32x2*>((uint16_t*)a.out + (int64_t)(begin + row) * a.ldout + col) =
-          u32x2{pack_half(fp16, v[0], v[1]), pack_half(fp16, v[2], v[3])};
+    };
+    const int tiles = (live + 15) / 16;
+    if (MT == 1 || tiles == 1)
+      body(std::integral_constant<int, 1>{});
+    else if (MT == 2 || tiles == 2)
+      body(std::integral_constant<int, MT < 2 ? 1 : 2>{});
+    else
+      body(std::integral_constant<int, MT>{});
+
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) part[wave][m * NC + c][lane] = acc[m][c];
+    __syncthreads();
+
+    // lane l of tile (m, c): row 16m + l % 16, columns 16c + 4 (l / 16) ..
+    const bool fp16 = T == Num::kFp16 || (T == Num::kInt8 && a.out_type == MOE_TYPE_FP16);
+    constexpr int kTiles = GATED ? MT : MT * NC;  // result tiles
+    for (int tile = wave; tile < kTiles; tile += kStreamWaves) {
+      const int m = GATED ? tile : tile / NC, c = GATED ? 0 : tile % NC;
+      const int row = 16 * m + l16, col = n0 + 16 * c + 4 * quad;
+      if (row >= live || col >= ncols) continue;
+      auto total = [&](int t, int up) -> f32x4 {
+        acc_t v = part[0][t][lane];
+#pragma unroll
+        for (int w = 1; w < kStreamWaves; ++w) v += part[w][t][lane];
+        f32x4 f;
+        if constexpr (T == Num::kInt8) {
+          const float ps = a.pscale[begin + row];
+          const f32x4 s = *reinterpret_cast<const f32x4*>(a.qscale + (int64_t)group * a.cols + (up ? F : 0) + col);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = (float)v[e] * ps * s[e];
+        } else {
+          f = v;
+        }
+        return f;
+      };
+      f32x4 v = total(GATED ? m * NC : tile, 0);
+      if constexpr (RES == Result::kWide) {
+        *reinterpret_cast<f32x4*>((float*)a.out + (int64_t)(begin + row) * a.ldout + col) = v;
+      } else {
+        if constexpr (GATED) {
+          const f32x4 u = total(m * NC + 1, 1);
+          if (T != Num::kInt8 && a.keep) {
+            uint16_t* k = a.keep + (int64_t)(begin + row) * a.ldkeep + col;
+            *reinterpret_cast<u32x2*>(k) = u32x2{pack_half(fp16, v[0], v[1]), pack_half(fp16, v[2], v[3])};
+            *reinterpret_cast<u32x2*>(k + F) = u32x2{pack_half(fp16, u[0], u[1]), pack_half(fp16, u[2], u[3])};
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = activate(a.act, v[e]) * u[e];
+        }
+        *reinterpret_cast<u32x2*>((uint16_t*)a.out + (int64_t)(begin + row) * a.ldout + col) =
+            u32x2{pack_half(fp16, v[0], v[1]), pack_half(fp16, v[2], v[3])};
+      }
     }
   }
 }
 
+// Blocks of `no` columns and 16 mt rows that have rows, at least: the offsets
+// are on the device.
+int64_t live_blocks(const ProductArgs& a, int ncols, int no, int mt) {
+  return (int64_t)((ncols + no - 1) / no) * std::max(a.groups, (a.rows + 16 * mt - 1) / (16 * mt));
+}
+
+constexpr int kFullChip = 256;
 template <Num T, Result RES, int NC>
 void launch_mt(const ProductArgs& a, hipStream_t s) {
   const int ncols = RES == Result::kGated ? a.cols / 2 : a.cols;
   const int no = RES == Result::kGated ? 16 : 16 * NC;
-  // row tiles of 16 of the largest possible group, up to 4 a block
-  const int mt = a.rows <= 16 ? 1 : a.rows <= 32 ? 2 : 4;
-  const dim3 grid((ncols + no - 1) / no, a.groups, (a.rows + 16 * mt - 1) / (16 * mt));
+  // row tiles of 16 of the largest possible group, up to 4 a block; fewer while
+  // that leaves compute units idle
+  int mt = a.rows <= 16 ? 1 : a.rows <= 32 ? 2 : 4;
+  while (mt > 1 && live_blocks(a, ncols, no, mt / 2) <= kFullChip) mt /= 2;
+  // a block for every row tile that a group might have; of the high blocks,
+  // which walk on over a group's tiles, four for each of an average group:
+  // blocks beyond a group's rows cost 0.7 ns each (1024 rows over 64 groups of
+  // 2048 gated columns of 4096, codes: 225 us with all of them, 203 without)
+  int tiles = (a.rows + 16 * mt - 1) / (16 * mt);
+  if (mt == 4 && a.groups > 1) tiles = std::min(tiles, 2 + 4 * tiles / a.groups);
+  const dim3 grid((ncols + no - 1) / no, a.groups, tiles);
   const int threads = 64 * kStreamWaves;
   if (mt == 1)
     product_stream_kernel<T, RES, 1, NC><<<grid, threads, 0, s>>>(a);
@@ -184,18 +221,12 @@ void launch_mt(const ProductArgs& a, hipStream_t s) {
     product_stream_kernel<T, RES, 4, NC><<<grid, threads, 0, s>>>(a);
 }
 
-// A block of 32 columns reads the rows half as often, one of 16 makes twice as
-// many blocks.  With more than 4 rows a group and blocks for most compute units
-// the wide ones win: 16 rows x 12800 columns of 4096 in bf16: 29.6 against 35.3
-// us; 256 rows over 16 groups of 4096 columns of 2048: 58 against 71; 16 x 6400
-// (200 blocks of 32): 18.2 against 19.8.  16 x 4096 of 14336 (128 blocks): 45
-// against 34; 96 rows over 64 groups, codes: 58 against 51.
 constexpr int kWideBlocks = 192, kWideRows = 4;
 template <Num T, Result RES>
 void launch_stream(const ProductArgs& a, hipStream_t s) {
   if constexpr (RES == Result::kGated)
     launch_mt<T, RES, 2>(a, s);
-  else if ((int64_t)a.groups * ((a.cols + 31) / 32) >= kWideBlocks && a.rows > kWideRows * a.groups)
+  else if (live_blocks(a, a.cols, 32, 1) >= kWideBlocks && a.rows > kWideRows * a.groups)
     launch_mt<T, RES, 2>(a, s);
   else
     launch_mt<T, RES, 1>(a, s);

@@ -121,6 +121,11 @@ FEW = [([1], 8, 8), ([1], 64, 4096), ([3], 1000, 72), ([16], 40, 136), ([17], 24
        ([64], 128, 520), ([0, 1, 0, 5, 16, 0, 7], 72, 200), ([20, 0, 44], 136, 328)]
 TILES = [([65], 8, 8), ([129], 136, 72), ([200], 1000, 1416), ([0, 70, 0, 1, 128, 255, 0], 264, 200),
          ([256, 300], 128, 64), ([1000], 392, 456), ([3, 130, 67], 1000, 2056)]
+# many groups with more rows than the streaming kernel takes: tiles at small widths; and uneven
+# groups of few rows on average, whose blocks walk over a group's row tiles
+MANY = [([150] + [0] * 8, 8, 16), ([0, 70, 0, 1, 128, 255, 0, 0, 0, 0], 264, 200), ([1000] + [0] * 8, 392, 464),
+        ([0] * 8 + [200], 1000, 1416), ([3, 130, 67] + [0] * 7, 1000, 2056), ([0, 300] + [0] * 8, 264, 8200),
+        ([0] * 20 + [700] + [3] * 30 + [0] * 13, 264, 80), ([1, 150] + [7] * 14, 1032, 520)]
 # past the streaming kernel: 128-wide blocks (whole, and with the contraction split), 256-wide ones (the
 # remainder of the last round split in the last)
 BIG = [([3700], 4096, 72), ([500, 0, 1, 1255, 129, 1100], 1000, 2056), ([2049], 520, 4104), ([4096], 4096, 72),
@@ -128,7 +133,7 @@ BIG = [([3700], 4096, 72), ([500, 0, 1, 1255, 129, 1100], 1000, 2056), ([2049], 
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("sizes,n,k", FEW + TILES + BIG, ids=str)
+@pytest.mark.parametrize("sizes,n,k", FEW + TILES + MANY + BIG, ids=str)
 def test_expert_product(torch, moe, sizes, n, k, dtype):
     say(f"expert_product {sizes} {n} {k} {dtype}")
     c = Case(torch, sizes, n, k, getattr(torch, dtype))
@@ -139,7 +144,7 @@ def test_expert_product(torch, moe, sizes, n, k, dtype):
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("sizes,n,k", FEW + TILES + BIG[1:], ids=str)
+@pytest.mark.parametrize("sizes,n,k", FEW + TILES + MANY + BIG[1:], ids=str)
 def test_gated_product(torch, moe, sizes, n, k, dtype, act):
     say(f"gated_product {sizes} {n} {k} {dtype} {act}")
     c = Case(torch, sizes, n, k, getattr(torch, dtype), wide=2)
@@ -230,7 +235,7 @@ def to16(cases):
 
 
 @pytest.mark.parametrize("dtype", TYPES + ["float32"])
-@pytest.mark.parametrize("sizes,n,k", to16(FEW + TILES + BIG), ids=str)
+@pytest.mark.parametrize("sizes,n,k", to16(FEW + TILES + MANY + BIG), ids=str)
 def test_int8_product(torch, moe, sizes, n, k, dtype):
     say(f"int8_product {sizes} {n} {k} {dtype}")
     c, y = int_case(torch, sizes, n, k, 1)
@@ -241,7 +246,7 @@ def test_int8_product(torch, moe, sizes, n, k, dtype):
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("sizes,n,k", to16(FEW + TILES + [BIG[1]]), ids=str)
+@pytest.mark.parametrize("sizes,n,k", to16(FEW + TILES + MANY + [BIG[1]]), ids=str)
 def test_int8_gated(torch, moe, sizes, n, k, dtype, act):
     say(f"int8_gated {sizes} {n} {k} {dtype} {act}")
     c, y = int_case(torch, sizes, n, k, 2)
@@ -577,12 +582,13 @@ def test_captured_calls_replay(torch, moe, rows):
 def test_two_graphs_share_a_workspace(torch, moe):
     """Graphs over one workspace, replayed one after the other, keep nothing in it between calls."""
     c = Case(torch, [1000], 256, 8192, torch.bfloat16)
-    d = Case(torch, [900], 192, 8192, torch.bfloat16, seed=1)
-    ws = torch.empty(max(moe.product_workspace("expert_product", 1000, 256, 8192),
-                         moe.product_workspace("expert_product", 900, 192, 8192)), dtype=torch.uint8, device="cuda")
-    assert ws.numel() > 0
+    d = Case(torch, [900], 1024, 8192, torch.bfloat16, seed=1)
+    needs = [moe.product_workspace("expert_product", 1000, 256, 8192),
+             moe.product_workspace("expert_product", 900, 1024, 8192)]
+    assert min(needs) > 0
+    ws = torch.empty(max(needs), dtype=torch.uint8, device="cuda")
     outs = [torch.empty(1000, 256, dtype=torch.bfloat16, device="cuda"),
-            torch.empty(900, 192, dtype=torch.bfloat16, device="cuda")]
+            torch.empty(900, 1024, dtype=torch.bfloat16, device="cuda")]
     refs = [moe.expert_product(c.x, c.w), moe.expert_product(d.x, d.w)]
     torch.cuda.synchronize()
     graphs = []

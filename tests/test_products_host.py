@@ -110,10 +110,10 @@ def test_forward_arguments_refused(lib, op):
     assert forward(lib, op, rows=4, ldout=66) == INVALID
     assert forward(lib, op, rows=4, groups=2) == INVALID         # groups without offsets
     assert forward(lib, op, rows=4, groups=2, offsets=FAKE + 2) == INVALID
-    assert forward(lib, op, rows=1000, n=256, k=8192, ws_bytes=1) == SMALL
+    assert forward(lib, op, rows=1000, n=1024, k=8192, ws_bytes=1) == SMALL
     assert "needs" in _lib.last_error()
-    assert forward(lib, op, rows=1000, n=256, k=8192, ws=None, ws_bytes=1 << 40) == INVALID
-    assert forward(lib, op, rows=1000, n=256, k=8192, ws=FAKE + 8) == INVALID
+    assert forward(lib, op, rows=1000, n=1024, k=8192, ws=None, ws_bytes=1 << 40) == INVALID
+    assert forward(lib, op, rows=1000, n=1024, k=8192, ws=FAKE + 8) == INVALID
     if op.startswith("int8"):
         assert forward(lib, op, rows=4, scale=None) == INVALID
         assert forward(lib, op, rows=4, w_scale=None) == INVALID
