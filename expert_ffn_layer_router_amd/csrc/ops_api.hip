@@ -337,12 +337,12 @@ MOE_EXPORT moe_status moe_quantize_rows(int32_t rows, int32_t k, int32_t type, c
                                         int8_t* codes, int64_t ldcodes, float* scale, moe_stream stream) {
   if (rows < 0 || rows > kMaxRows)
     return api_fail(MOE_ERR_UNSUPPORTED_SHAPE, "rows=%d outside [0, %d]", rows, kMaxRows);
-  if (k < 16 || k > kMaxWidth || k % 16)
-    return api_fail(MOE_ERR_UNSUPPORTED_SHAPE, "k=%d must be a multiple of 16 in [16, %d]", k, kMaxWidth);
+  if (k < 8 || k > kMaxWidth || k % 8)
+    return api_fail(MOE_ERR_UNSUPPORTED_SHAPE, "k=%d must be a multiple of 8 in [8, %d]", k, kMaxWidth);
   if (type != MOE_TYPE_BF16 && type != MOE_TYPE_FP16)
     return api_fail(MOE_ERR_UNSUPPORTED_SHAPE, "type=%d must be bf16 or fp16", type);
   MOE_TRY(check_rows("x", x, ldx, rows, k, 8));
-  MOE_TRY(check_rows("codes", codes, ldcodes, rows, k, 16));
+  MOE_TRY(check_rows("codes", codes, ldcodes, rows, k, 8));
   if (rows == 0) return MOE_OK;
   MOE_TRY(check_plain("scale", scale));
   launch_quantize(rows, k, type, x, ldx, codes, ldcodes, scale, static_cast<hipStream_t>(stream));

@@ -9,7 +9,7 @@ outside every group are not read, and their outputs are left as they were (in
 a result that the call allocates: unspecified).
 
 Row matrices may have any row stride that is a multiple of 8 elements (16 for
-codes); weights, scales and offsets are contiguous.  A call runs on `stream`
+a product's codes); weights, scales and offsets are contiguous.  A call runs on `stream`
 (default: the current stream of the tensors' device) and allocates what it is
 not given there; with `out` and `workspace` given it allocates nothing.  On
 another stream than the current one the caller orders the call after what

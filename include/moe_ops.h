@@ -25,8 +25,8 @@
  *     argument checks before anything is enqueued, no device allocation, work
  *     on `stream` only (of the current device), no host synchronisation.
  *   - `ld...` arguments are row strides in elements; they are multiples of 8
- *     (of 16 for codes), at least the row's length and at most 2^20.  Pointers
- *     are 16-byte aligned.  Weights, their scales and dw are contiguous.
+ *     (of 16 for the products' codes), at least the row's length and at most
+ *     2^20.  Pointers are 16-byte aligned.  Weights, their scales and dw are contiguous.
  *     Outputs overlap no other argument.
  *   - offsets: device int32 [groups + 1], ascending, within 0 .. rows, read
  *     when the kernels run; NULL with one group means all rows.  Rows outside
@@ -87,7 +87,8 @@ moe_status moe_product_workspace(const moe_product *p, moe_op op, size_t *bytes)
  * [rows][k] in -127 .. 127, scale fp32 [rows].  The rounding is that of the
  * exact quotient, ties to even.  A row of zeros has scale 0; a row with an
  * infinity or NaN has scale NaN and codes 0 (its products are NaN).
- * k is a multiple of 16 in 16 .. 65536, rows 0 .. 2^22. */
+ * k is a multiple of 8 in 8 .. 65536 and so is ldcodes (the products take
+ * codes in 16s), rows 0 .. 2^22. */
 moe_status moe_quantize_rows(int32_t rows, int32_t k, int32_t type, const uint16_t *x, int64_t ldx, int8_t *codes,
                              int64_t ldcodes, float *scale, moe_stream stream);
 

@@ -281,7 +281,8 @@ def quantize64(torch, x):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,k", [(1, 16), (3, 64), (5, 1008), (7, 1024), (2, 1040), (16, 4096), (3, 4112), (33, 14336),
-                                    (2, 16384), (3, 20000), (1, 65536)])
+                                    (2, 16384), (3, 20000), (1, 65536), (3, 8), (5, 24), (3, 1032), (4, 4104),
+                                    (2, 16392), (1, 65528)])
 def test_quantize_rows(torch, moe, rows, k, dtype):
     gen = torch.Generator(device="cuda").manual_seed(rows + k)
     t = getattr(torch, dtype)

@@ -165,11 +165,11 @@ def test_quantize_arguments_refused(lib):
 
     assert call(rows=0) == 0
     assert call(rows=0, x=None, codes=None, scale=None) == 0
-    for kw in (dict(rows=-1), dict(rows=(1 << 22) + 1), dict(k=0), dict(k=8), dict(k=24), dict(k=65552),
+    for kw in (dict(rows=-1), dict(rows=(1 << 22) + 1), dict(k=0), dict(k=4), dict(k=20), dict(k=65544),
                dict(type_=FP32), dict(type_=-1)):
         assert call(**kw) == SHAPE, kw
     for kw in (dict(x=None), dict(x=FAKE + 2), dict(ldx=56), dict(ldx=68), dict(codes=None), dict(codes=FAKE + 8),
-               dict(ldc=48), dict(ldc=72), dict(scale=None), dict(scale=FAKE + 2)):
+               dict(ldc=48), dict(ldc=56), dict(ldc=68), dict(scale=None), dict(scale=FAKE + 2)):
         assert call(**kw) == INVALID, kw
 
 
