@@ -8,16 +8,27 @@
 // and nothing is reused through LDS.  kRun steps are loaded while the previous
 // kRun are multiplied; a wave's steps are consecutive, so that it reads
 // kilobytes of each row in turn.  The rows come from the caches in the same
-// fragment layout.  The waves' sums meet in LDS and are added in wave order, so
-// the result does not depend on timing.
+// way.  The waves' sums meet in LDS and are added in wave order, so the result
+// does not depend on timing.
 //
-// 32 rows over 8 groups of 14336 gated columns of 4096 codes: 158 us, 5.9 TB/s
+// A load is 16 bytes a lane of 16 rows.  The matrix cores want row l % 16 in
+// lane l, but the address unit takes four neighbouring lanes at a time, and if
+// these ask for four rows it looks up four lines for 64 bytes: 16 bytes a clock
+// and compute unit, which bounded blocks of more rows (64 rows x 1024 columns
+// of 4096 in bf16: 21.5 us).  So four neighbours load 64 bytes of one row, and
+// each fragment is exchanged between the lanes afterwards (ds_bpermute: LDS's
+// crossbar, none of its memory): 14.7 us, with 16-row blocks 8.6.  Whole
+// 128-byte lines (eight lanes a row, two more moves a fragment) gained 6% where
+// memory is the bound (16 x 12800 of 4096: 25.1 against 26.6) and lost 10-25%
+// elsewhere; 8 waves a block: 28.3 -> 29.5 at 16 x 4096 of 14336, 16 x 8192 of
+// 4096: 17.0 -> 19.0.
+//
+// 32 rows over 8 groups of 14336 gated columns of 4096 codes: 160 us, 5.9 TB/s
 // (a read-only stream reaches 6.7); 16 rows x one group of 6400 gated columns
-// of 4096 in bf16: 25 us, 4.2 TB/s: 400 blocks, whose start and end show.
-// Eight waves dealt runs of four steps in turn took 221 us for the first:
-// what counts is how many consecutive bytes of a row a wave asks for.  The
-// non-temporal hint, which drops a line's second half before it is asked for,
-// cost 15%.
+// of 4096 in bf16: 25.8 us from memory (4.1 TB/s: 400 blocks, whose start and
+// end show), 19.4 from the last-level cache.
+// The non-temporal hint, which drops a line's second half before it is asked
+// for, cost 15%.
 #include <type_traits>
 
 #include "product_core.h"
@@ -196,6 +207,9 @@ int64_t live_blocks(const ProductArgs& a, int ncols, int no, int mt) {
   return (int64_t)((ncols + no - 1) / no) * std::max(a.groups, (a.rows + 16 * mt - 1) / (16 * mt));
 }
 
+// 64 rows x 256 columns of 4096 in bf16: blocks of 16 rows 8.1 us, of 64 14.5;
+// 64 x 2048 (256 blocks of 32 rows): 11.2 against 11.5 with 512 of 16; 64 x
+// 6400 (200 blocks of 64 rows and 32 columns): 24.4 against 25.9 with 32 rows.
 constexpr int kFullChip = 256;
 template <Num T, Result RES, int NC>
 void launch_mt(const ProductArgs& a, hipStream_t s) {
@@ -221,6 +235,13 @@ void launch_mt(const ProductArgs& a, hipStream_t s) {
     product_stream_kernel<T, RES, 4, NC><<<grid, threads, 0, s>>>(a);
 }
 
+// A block of 32 columns reads the rows half as often, one of 16 makes twice as
+// many blocks.  With more than 4 rows a group and blocks for most compute units
+// the wide ones win: 64 rows x 4096 columns of 4096 in bf16: 13.9 against 15.8
+// us; 128 x 4096 codes of 4096: 12.0 against 15.6; 16 x 12800: 26.6 against
+// 28.8; 256 over 16 groups of 4096 columns of 2048: 54.8 against 58.7.  16 x
+// 4096 of 14336 (128 blocks): 40.5 against 29.1; 64 x 1024 of 4096 (128): 10.7
+// against 8.6.
 constexpr int kWideBlocks = 192, kWideRows = 4;
 template <Num T, Result RES>
 void launch_stream(const ProductArgs& a, hipStream_t s) {
