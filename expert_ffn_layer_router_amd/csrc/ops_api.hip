@@ -405,7 +405,7 @@ MOE_EXPORT moe_status moe_gated_product_backward(const moe_product* p, const uin
   uint16_t* dgu = static_cast<uint16_t*>(workspace);
   const int wide = 2 * p->n;
   if ((dx || dw) && p->rows > 0) {
-    launch_gated_slopes(p->rows, p->n, p->type, p->activation, dh, lddh, gate_up, ldgate_up, dgu, s);
+    launch_gated_slopes(p->rows, p->n, p->type, p->activation, dh, lddh, gate_up, ldgate_up, offsets, p->groups, dgu, s);
     MOE_TRY(check_launch());
   }
   return gradients(p, wide, dgu, wide, x, ldx, w, offsets, dx, lddx, dw, dw_type,

@@ -100,15 +100,20 @@ __global__ __launch_bounds__(256) void quantize_kernel(int rows, int k, bool fp1
 // ---- slopes of the gated block ------------------------------------------------
 // dg = dh u act'(g), du = dh act(g); 8 columns per thread.  Bound by memory:
 // 10 bytes per element of dh (4096 rows of 14336: 93-117 us, 5.0-6.3 TB/s).
+// Rows before the first group and behind the last are skipped: nothing reads
+// their slopes, and a captured call may have many spare rows.
 __global__ __launch_bounds__(256) void gated_slopes_kernel(int rows, int n, bool fp16, int act,
                                                            const uint16_t* __restrict__ dh, int64_t lddh,
                                                            const uint16_t* __restrict__ gu, int64_t ldgu,
+                                                           const int32_t* __restrict__ offsets, int groups,
                                                            uint16_t* __restrict__ dgu) {
   const int per_row = n / 8;
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t row = at / per_row;
   const int col = (int)(at % per_row) * 8;
-  if (row >= rows) return;
+  const int first = offsets ? max(offsets[0], 0) : 0;
+  const int last = offsets ? min(offsets[groups], rows) : rows;
+  if (row < first || row >= last) return;
   const u32x4 d = *reinterpret_cast<const u32x4*>(dh + row * lddh + col);
   const u32x4 g = *reinterpret_cast<const u32x4*>(gu + row * ldgu + col);
   const u32x4 u = *reinterpret_cast<const u32x4*>(gu + row * ldgu + n + col);
@@ -153,10 +158,10 @@ void launch_quantize(int rows, int k, int type, const uint16_t* x, int64_t ldx, 
 }
 
 void launch_gated_slopes(int rows, int n, int type, int act, const uint16_t* dh, int64_t lddh, const uint16_t* gate_up,
-                         int64_t ldgu, uint16_t* dgu, hipStream_t s) {
+                         int64_t ldgu, const int32_t* offsets, int groups, uint16_t* dgu, hipStream_t s) {
   const int64_t threads = (int64_t)rows * (n / 8);
   gated_slopes_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(rows, n, type == MOE_TYPE_FP16, act, dh, lddh,
-                                                                        gate_up, ldgu, dgu);
+                                                                        gate_up, ldgu, offsets, groups, dgu);
 }
 
 }  // namespace moe

@@ -69,8 +69,8 @@ void launch_product_grad(const ProductArgs& a, const ProductPlan& p, Num num, Pa
 void launch_product_stream(const ProductArgs& a, Num num, Result res, hipStream_t s);
 void launch_quantize(int rows, int k, int type, const uint16_t* x, int64_t ldx, int8_t* codes, int64_t ldcodes,
                      float* scale, hipStream_t s);
-// (dg, du) [rows][2n] from dh [rows][n] and the saved (g, u)
+// (dg, du) [rows][2n] of the groups' rows from dh [rows][n] and the saved (g, u)
 void launch_gated_slopes(int rows, int n, int type, int act, const uint16_t* dh, int64_t lddh, const uint16_t* gate_up,
-                         int64_t ldgu, uint16_t* dgu, hipStream_t s);
+                         int64_t ldgu, const int32_t* offsets, int groups, uint16_t* dgu, hipStream_t s);
 
 }  // namespace moe

@@ -19,7 +19,7 @@ from test_gpu_products import moe, torch  # noqa: F401  (fixtures)
 
 pytestmark = pytest.mark.gpu
 
-WIDE_TILE, SMALL_TILE = 256 * 256 * 4, 128 * 128 * 4  # bytes of one part's raw sums
+WIDE_TILE = 256 * 256 * 4  # bytes of one part's raw sums
 
 
 def sentinel(torch, need):
@@ -315,3 +315,24 @@ def test_replays_follow_rewritten_inputs(torch, moe, sizes, n, k):
                     assert torch.equal(a[ends[0]:ends[-1]], b[ends[0]:ends[-1]]), (op, turn)
                     assert (a[:ends[0]] == 3).all() and (a[ends[-1]:] == 3).all(), (op, turn)
         del graph
+
+
+# ---- rows of no group ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("sizes,before,after", [([5, 0, 9], 3, 6), ([0, 0, 0], 8, 8), ([40, 1, 200], 0, 100), ([], 0, 0)], ids=str)
+def test_slopes_of_rows_of_no_group_are_not_computed(torch, moe, sizes, before, after, dtype):
+    """The gated backward pass neither reads nor writes anything for rows before and behind the groups: the
+    workspace, which starts with (dg, du) of each row, keeps what stood there."""
+    n, k = 72, 64
+    if not sizes:  # one group without offsets has all rows
+        c = Case(torch, [17], n, k, getattr(torch, dtype), wide=2, offsets=False)
+    else:
+        c = Case(torch, sizes, n, k, getattr(torch, dtype), wide=2, before=before, after=after)
+    m = c.member()
+    dh, gu = c.normal(c.rows, n), c.normal(c.rows, 2 * n)
+    ws = sentinel(torch, moe.product_workspace("gated_product_backward", c.rows, n, k, len(c.sizes), dtype=c.dtype))
+    moe.gated_product_backward(dh, gu, c.x, c.w, c.offsets, workspace=ws)
+    pairs = ws[: c.rows * 4 * n].view(c.rows, 4 * n)
+    assert (pairs[~m] == 0xA5).all()
+    assert (pairs[m] != 0xA5).any(1).all()
