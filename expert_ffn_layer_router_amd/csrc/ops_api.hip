@@ -203,6 +203,12 @@ Result forward_result(const moe_product* p, bool gated) {
   return gated ? Result::kGated : p->type == MOE_TYPE_FP32 ? Result::kWide : Result::kHalf;
 }
 
+// The gated backward pass's (dg, du), and in fp16 each group's largest behind them.
+size_t slopes_only_bytes(const moe_product* p) { return align_up((size_t)p->rows * 2 * p->n * 2); }
+size_t slopes_bytes(const moe_product* p) {
+  return slopes_only_bytes(p) + (p->type == MOE_TYPE_FP16 && p->rows > 0 ? align_up(p->groups * sizeof(uint32_t)) : 0);
+}
+
 size_t workspace_bytes_of(const moe_product* p, moe_op op) {
   const bool codes = op == MOE_OP_INT8_PRODUCT || op == MOE_OP_INT8_GATED;
   const Num num = codes ? Num::kInt8 : half_num(p);
@@ -220,7 +226,7 @@ size_t workspace_bytes_of(const moe_product* p, moe_op op) {
       const int wide = gated ? 2 * p->n : p->n;
       const size_t dx = plan_product(num, Pass::kInputGrad, Result::kHalf, input_grad_args(p, wide)).partial_bytes;
       const size_t dw = plan_product(num, Pass::kWeightGrad, Result::kHalf, weight_grad_args(p, wide)).partial_bytes;
-      return std::max(dx, dw) + (gated ? align_up((size_t)p->rows * wide * 2) : 0);
+      return std::max(dx, dw) + (gated ? slopes_bytes(p) : 0);
     }
   }
 }
@@ -288,10 +294,10 @@ moe_status check_backward(const moe_product* p, const uint16_t* x, int64_t ldx, 
   return check_offsets(p, offsets);
 }
 
-// dx and dw of a product whose outputs' gradient is dy [rows][wide]
+// dx and dw of a product whose outputs' gradient is dy [rows][wide] (tops: ProductArgs)
 moe_status gradients(const moe_product* p, int wide, const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
                      const uint16_t* w, const int32_t* offsets, uint16_t* dx, int64_t lddx, void* dw, int32_t dw_type,
-                     char* partial, hipStream_t s) {
+                     const uint32_t* tops, char* partial, hipStream_t s) {
   const Num num = half_num(p);
   if (dx && p->rows > 0) {
     ProductArgs a = input_grad_args(p, wide);
@@ -301,6 +307,7 @@ moe_status gradients(const moe_product* p, int wide, const uint16_t* dy, int64_t
     a.q = reinterpret_cast<const char*>(w);
     a.offsets = offsets;
     a.out = dx;
+    a.tops = tops;
     a.ldout = lddx;
     enqueue(a, plan, num, Pass::kInputGrad, Result::kHalf, partial, s);
     MOE_TRY(check_launch());
@@ -315,6 +322,7 @@ moe_status gradients(const moe_product* p, int wide, const uint16_t* dy, int64_t
     a.ldq = ldx * 2;
     a.offsets = offsets;
     a.out = dw;
+    a.tops = tops;
     enqueue(a, plan, num, Pass::kWeightGrad, res, partial, s);
     MOE_TRY(check_launch());
   }
@@ -386,8 +394,8 @@ MOE_EXPORT moe_status moe_expert_product_backward(const moe_product* p, const ui
   MOE_TRY(check_rows("dy", dy, lddy, p->rows, p->n, 8));
   MOE_TRY(check_backward(p, x, ldx, w, offsets, dx, lddx, dw, dw_type));
   MOE_TRY(check_workspace(workspace, workspace_bytes, workspace_bytes_of(p, MOE_OP_EXPERT_PRODUCT_BACKWARD)));
-  return gradients(p, p->n, dy, lddy, x, ldx, w, offsets, dx, lddx, dw, dw_type, static_cast<char*>(workspace),
-                   static_cast<hipStream_t>(stream));
+  return gradients(p, p->n, dy, lddy, x, ldx, w, offsets, dx, lddx, dw, dw_type, nullptr,
+                   static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
 }
 
 MOE_EXPORT moe_status moe_gated_product_backward(const moe_product* p, const uint16_t* dh, int64_t lddh,
@@ -401,13 +409,17 @@ MOE_EXPORT moe_status moe_gated_product_backward(const moe_product* p, const uin
   MOE_TRY(check_backward(p, x, ldx, w, offsets, dx, lddx, dw, dw_type));
   MOE_TRY(check_workspace(workspace, workspace_bytes, workspace_bytes_of(p, MOE_OP_GATED_PRODUCT_BACKWARD)));
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  // (dg, du) first in the workspace, then the parts of a split contraction
+  // (dg, du) first in the workspace, then the groups' largest, then the parts of a split contraction
   uint16_t* dgu = static_cast<uint16_t*>(workspace);
+  uint32_t* tops = nullptr;
+  if (p->type == MOE_TYPE_FP16 && p->rows > 0)
+    tops = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + slopes_only_bytes(p));
   const int wide = 2 * p->n;
   if ((dx || dw) && p->rows > 0) {
-    launch_gated_slopes(p->rows, p->n, p->type, p->activation, dh, lddh, gate_up, ldgate_up, offsets, p->groups, dgu, s);
+    launch_gated_slopes(p->rows, p->n, p->type, p->activation, dh, lddh, gate_up, ldgate_up, offsets, p->groups, dgu,
+                        tops, s);
     MOE_TRY(check_launch());
   }
-  return gradients(p, wide, dgu, wide, x, ldx, w, offsets, dx, lddx, dw, dw_type,
-                   static_cast<char*>(workspace) + align_up((size_t)p->rows * wide * 2), s);
+  return gradients(p, wide, dgu, wide, x, ldx, w, offsets, dx, lddx, dw, dw_type, tops,
+                   static_cast<char*>(workspace) + slopes_bytes(p), s);
 }

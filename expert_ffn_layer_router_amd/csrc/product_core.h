@@ -72,6 +72,13 @@ __device__ __forceinline__ void activate_slope(int act, float g, float& value, f
   slope = fmaf(g * sig * rest, s.dz, sig) * unit;
 }
 
+// The power of two that a group's fp16 slopes were divided by, from the bits of
+// the largest (0: none passes 65504): that one is in [2^14, 2^15) afterwards.
+constexpr float kHalfMax = 65504.0f;
+__device__ __forceinline__ float group_lift(uint32_t top) {
+  return top ? __builtin_amdgcn_ldexpf(1.0f, __builtin_amdgcn_frexp_expf(__uint_as_float(top)) - 15) : 1.0f;
+}
+
 // 16 x 16 of A (lane l: row l % 16, 16 bytes of the contraction at
 // 16 (l / 16)) times B (the same for its columns): D holds column l % 16, rows
 // 4 (l / 16) + i.
@@ -612,6 +619,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
 #pragma unroll
       for (int i = 0; i < MI; ++i) prow[i] = rowl(i) < live ? a.pscale[row0 + rowl(i)] : 0.0f;
     }
+    // the gated block's fp16 slopes may stand divided by a power of two
+    constexpr bool LIFT = T == Num::kFp16 && PASS != Pass::kForward;
+    const float lift = LIFT && a.tops ? group_lift(a.tops[group]) : 1.0f;
     const float* qs = T == Num::kInt8 ? a.qscale + (int64_t)group * a.cols : nullptr;
     auto value = [&](int i, int j) -> f32x4 {
       f32x4 v;
@@ -622,6 +632,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
         for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][j][e] * prow[i] * s[e];
       } else {
         v = acc[i][j];
+        if constexpr (LIFT) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] *= lift;
+        }
       }
       return v;
     };

@@ -1,5 +1,6 @@
 // The element-wise parts of the grouped products: quantising rows and the
 // gated block's slopes.
+#include <algorithm>
 #include <type_traits>
 
 #include "product_core.h"
@@ -102,21 +103,19 @@ __global__ __launch_bounds__(256) void quantize_kernel(int rows, int k, bool fp1
 // 10 bytes per element of dh (4096 rows of 14336: 93-117 us, 5.0-6.3 TB/s).
 // Rows before the first group and behind the last are skipped: nothing reads
 // their slopes, and a captured call may have many spare rows.
-__global__ __launch_bounds__(256) void gated_slopes_kernel(int rows, int n, bool fp16, int act,
-                                                           const uint16_t* __restrict__ dh, int64_t lddh,
-                                                           const uint16_t* __restrict__ gu, int64_t ldgu,
-                                                           const int32_t* __restrict__ offsets, int groups,
-                                                           uint16_t* __restrict__ dgu) {
-  const int per_row = n / 8;
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = at / per_row;
-  const int col = (int)(at % per_row) * 8;
-  const int first = offsets ? max(offsets[0], 0) : 0;
-  const int last = offsets ? min(offsets[groups], rows) : rows;
-  if (row < first || row >= last) return;
-  const u32x4 d = *reinterpret_cast<const u32x4*>(dh + row * lddh + col);
-  const u32x4 g = *reinterpret_cast<const u32x4*>(gu + row * ldgu + col);
-  const u32x4 u = *reinterpret_cast<const u32x4*>(gu + row * ldgu + n + col);
+//
+// They are operands of 16-bit matrix products and rounded to that type.  In
+// fp16 a product of finite values may pass 65504, where dx and dw do not: the
+// largest such slope of each group is kept (tops, 0 without one; the maximum
+// does not depend on the order), gated_slopes_far_kernel writes that group's
+// again, divided by the power of two group_lift, and the products' epilogues
+// multiply it back.  That costs the group's smaller slopes 2^-25 of the lift
+// (half of the smallest subnormal) and nothing where no slope is that large.
+__device__ __forceinline__ void slopes8(bool fp16, int act, int n, const uint16_t* dh, const uint16_t* gu, uint16_t* dgu,
+                                        float unit, float& far) {
+  const u32x4 d = *reinterpret_cast<const u32x4*>(dh);
+  const u32x4 g = *reinterpret_cast<const u32x4*>(gu);
+  const u32x4 u = *reinterpret_cast<const u32x4*>(gu + n);
   u32x4 og, ou;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -130,12 +129,73 @@ __global__ __launch_bounds__(256) void gated_slopes_kernel(int rows, int n, bool
       activate_slope(act, gv, value, slope);
       a[h] = dv * uv * slope;
       b[h] = dv * value;
+      if (fp16) {
+        // infinities and NaN of the inputs are no large slopes
+        const float ma = fabsf(a[h]), mb = fabsf(b[h]);
+        if (ma > kHalfMax && ma < __builtin_inff()) far = fmaxf(far, ma);
+        if (mb > kHalfMax && mb < __builtin_inff()) far = fmaxf(far, mb);
+        a[h] *= unit;
+        b[h] *= unit;
+      }
     }
     og[i] = pack_half(fp16, a[0], a[1]);
     ou[i] = pack_half(fp16, b[0], b[1]);
   }
-  *reinterpret_cast<u32x4*>(dgu + row * 2 * n + col) = og;
-  *reinterpret_cast<u32x4*>(dgu + row * 2 * n + n + col) = ou;
+  *reinterpret_cast<u32x4*>(dgu) = og;
+  *reinterpret_cast<u32x4*>(dgu + n) = ou;
+}
+
+__global__ __launch_bounds__(256) void clear_tops_kernel(uint32_t* tops, int groups) {
+  if ((int)threadIdx.x < groups) tops[threadIdx.x] = 0;
+}
+
+__global__ __launch_bounds__(256) void gated_slopes_kernel(int rows, int n, bool fp16, int act,
+                                                           const uint16_t* __restrict__ dh, int64_t lddh,
+                                                           const uint16_t* __restrict__ gu, int64_t ldgu,
+                                                           const int32_t* __restrict__ offsets, int groups,
+                                                           uint16_t* __restrict__ dgu, uint32_t* tops) {
+  const int per_row = n / 8;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = at / per_row;
+  const int col = (int)(at % per_row) * 8;
+  const int first = offsets ? max(offsets[0], 0) : 0;
+  const int last = offsets ? min(offsets[groups], rows) : rows;
+  if (row < first || row >= last) return;
+  float far = 0.0f;
+  slopes8(fp16, act, n, dh + row * lddh + col, gu + row * ldgu + col, dgu + row * 2 * n + col, 1.0f, far);
+  if (far > 0.0f) {
+    int e = 0;  // the row's group: the last that begins at or before it
+    if (offsets)
+      for (int past = groups; past - e > 1;) {
+        const int mid = (e + past) / 2;
+        if (offsets[mid] <= row) e = mid;
+        else past = mid;
+      }
+    // positive floats order as their bits; most threads find a larger one there
+    const uint32_t bits = __float_as_uint(far);
+    if (__hip_atomic_load(tops + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < bits) atomicMax(tops + e, bits);
+  }
+}
+
+__global__ __launch_bounds__(256) void gated_slopes_far_kernel(int rows, int n, int act, const uint16_t* __restrict__ dh,
+                                                               int64_t lddh, const uint16_t* __restrict__ gu,
+                                                               int64_t ldgu, const int32_t* __restrict__ offsets,
+                                                               uint16_t* __restrict__ dgu,
+                                                               const uint32_t* __restrict__ tops) {
+  const int group = blockIdx.y;
+  const uint32_t top = tops[group];
+  if (top == 0) return;
+  const float unit = 1.0f / group_lift(top);  // exact
+  int begin, end;
+  group_rows(offsets, rows, group, begin, end);
+  const int per_row = n / 8;
+  const int64_t chunks = (int64_t)(end - begin) * per_row;
+  for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < chunks; at += (int64_t)gridDim.x * 256) {
+    const int64_t row = begin + at / per_row;
+    const int col = (int)(at % per_row) * 8;
+    float far = 0.0f;
+    slopes8(true, act, n, dh + row * lddh + col, gu + row * ldgu + col, dgu + row * 2 * n + col, unit, far);
+  }
 }
 
 }  // namespace
@@ -158,10 +218,16 @@ void launch_quantize(int rows, int k, int type, const uint16_t* x, int64_t ldx, 
 }
 
 void launch_gated_slopes(int rows, int n, int type, int act, const uint16_t* dh, int64_t lddh, const uint16_t* gate_up,
-                         int64_t ldgu, const int32_t* offsets, int groups, uint16_t* dgu, hipStream_t s) {
+                         int64_t ldgu, const int32_t* offsets, int groups, uint16_t* dgu, uint32_t* tops, hipStream_t s) {
   const int64_t threads = (int64_t)rows * (n / 8);
-  gated_slopes_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(rows, n, type == MOE_TYPE_FP16, act, dh, lddh,
-                                                                        gate_up, ldgu, offsets, groups, dgu);
+  const unsigned blocks = (unsigned)((threads + 255) / 256);
+  if (tops) clear_tops_kernel<<<1, 256, 0, s>>>(tops, groups);
+  gated_slopes_kernel<<<blocks, 256, 0, s>>>(rows, n, type == MOE_TYPE_FP16, act, dh, lddh, gate_up, ldgu, offsets, groups,
+                                             dgu, tops);
+  // seldom more than a look at tops: few blocks, which walk over the group
+  if (tops)
+    gated_slopes_far_kernel<<<dim3(std::min(blocks, std::max(16u, 1024u / groups)), groups), 256, 0, s>>>(
+        rows, n, act, dh, lddh, gate_up, ldgu, offsets, dgu, tops);
 }
 
 }  // namespace moe

@@ -34,6 +34,9 @@ struct ProductArgs {
   const float* pscale = nullptr;   // codes: scale of each row, of each w row ([groups][cols])
   const float* qscale = nullptr;
   int act = 0;
+  // fp16 gradients of the gated block, or null: bits of each group's largest
+  // slope if it passes 65504 (P then holds the slopes over group_lift), else 0
+  const uint32_t* tops = nullptr;
   // contraction split: weight gradient, into this many parts; otherwise the
   // most parts that the kernels may choose (rounds_of), 1 if none can pay.
   // The parts' raw sums go to `partial`; a second launch joins them.
@@ -69,8 +72,9 @@ void launch_product_grad(const ProductArgs& a, const ProductPlan& p, Num num, Pa
 void launch_product_stream(const ProductArgs& a, Num num, Result res, hipStream_t s);
 void launch_quantize(int rows, int k, int type, const uint16_t* x, int64_t ldx, int8_t* codes, int64_t ldcodes,
                      float* scale, hipStream_t s);
-// (dg, du) [rows][2n] of the groups' rows from dh [rows][n] and the saved (g, u)
+// (dg, du) [rows][2n] of the groups' rows from dh [rows][n] and the saved (g, u);
+// fp16: tops [groups] receives what ProductArgs::tops says, else it is null
 void launch_gated_slopes(int rows, int n, int type, int act, const uint16_t* dh, int64_t lddh, const uint16_t* gate_up,
-                         int64_t ldgu, const int32_t* offsets, int groups, uint16_t* dgu, hipStream_t s);
+                         int64_t ldgu, const int32_t* offsets, int groups, uint16_t* dgu, uint32_t* tops, hipStream_t s);
 
 }  // namespace moe

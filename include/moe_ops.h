@@ -127,7 +127,11 @@ moe_status moe_gated_product(const moe_product *p, const uint16_t *x, int64_t ld
 
 /* dh [R][n], gate_up [R][2n] from the forward call; the rest as for
  * moe_expert_product_backward with w and dw [G][2n][k].  (dg, du) are rounded
- * to p->type between the two steps. */
+ * to p->type between the two steps.  In fp16 a group with one past 65504 has
+ * them divided by a power of two s before, so that the largest is in 2^14 ..
+ * 2^15, and the fp32 sums multiplied by s: its smaller ones are then off by up
+ * to s 2^-25 beside the rounding, and dx and dw are infinite only where they
+ * pass 65504 themselves. */
 moe_status moe_gated_product_backward(const moe_product *p, const uint16_t *dh, int64_t lddh,
                                       const uint16_t *gate_up, int64_t ldgate_up, const uint16_t *x, int64_t ldx,
                                       const uint16_t *w, const int32_t *offsets, uint16_t *dx, int64_t lddx, void *dw,

@@ -336,3 +336,124 @@ def test_slopes_of_rows_of_no_group_are_not_computed(torch, moe, sizes, before, 
     pairs = ws[: c.rows * 4 * n].view(c.rows, 4 * n)
     assert (pairs[~m] == 0xA5).all()
     assert (pairs[m] != 0xA5).any(1).all()
+
+
+# ---- gradients past the range of 16 bits -----------------------------------------------------
+
+def lifts(torch, c, d, dtype):
+    """Per row, the power of two that a group's (dg, du) are divided by: 1 unless one of them leaves fp16."""
+    lift = torch.ones(c.rows, 1, dtype=torch.float64, device="cuda")
+    for e, b, t in c.groups():
+        top = d[b:t][d[b:t].isfinite()].abs().max().item()
+        if dtype == torch.float16 and top > 60000:  # (at the border either is right: the larger one bounds both)
+            lift[b:t] = 2.0 ** max(0, torch.frexp(torch.tensor(top * 1.001))[1].item() - 15)
+    return lift
+
+
+def far_out(torch, c, n, rows, size):
+    """dh and (g, u) whose product passes 65504 in some rows; small x and w keep dx and dw inside."""
+    dh, gu = c.normal(c.rows, n), c.normal(c.rows, 2 * n)
+    dh[rows] *= size
+    gu[rows, n:] *= size
+    gu[rows, :n] *= 2
+    c.x.mul_(2.0 ** -8)
+    c.w.mul_(2.0 ** -8)
+    return dh, gu
+
+
+def check_range(torch, got, ref, bound, dtype, what):
+    """Within the bound where the value lies in the type's range, infinite (of its sign) where it is past it: a
+    64-bit result that is itself past 65504 + 16 rounds to infinity."""
+    edge = torch.finfo(dtype).max * (1 + torch.finfo(dtype).eps / 4)
+    past = ref.abs() - bound > edge
+    assert torch.equal(got[past].double(), ref[past].sign() * float("inf")), what
+    inside = ref.abs() + bound < edge
+    check(torch, got[inside], ref[inside], bound[inside], what)
+    return inside
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("size", [100.0, 300.0, 2000.0])
+@pytest.mark.parametrize("sizes,n,k", [([70, 0, 33], 72, 136), ([333, 0, 1, 667], 1032, 256), ([700, 1500, 600], 2056, 520)], ids=str)
+def test_gated_backward_past_65504(torch, moe, sizes, n, k, size, dtype, act):
+    """dh u act'(g) and dh act(g) of finite fp16 values may pass the largest fp16 number; dx and dw do not.
+    Those of a group are then divided by a power of two s before they are rounded, and the sums multiplied by it:
+    an error of half a step, 2^-11 relative, and s times half of the smallest subnormal (2^-25)."""
+    t = getattr(torch, dtype)
+    c = Case(torch, sizes, n, k, t, wide=2, after=2)
+    rows = torch.arange(1, sizes[0], 7, device="cuda")
+    dh, gu = far_out(torch, c, n, rows, size)
+    d, off = slopes64(torch, act, dh, gu, n, t)
+    lift = lifts(torch, c, d, t)
+    if t == torch.float16 and size >= 300:
+        assert lift[0] > 1 and lift[c.ends[-2]] == 1  # only the first group
+    off = off + 2.0 ** -25 * lift
+    dx, dw, dx_off, dw_off = grads64(torch, c, d, off)
+    got_dx, got_dw = moe.gated_product_backward(dh, gu, c.x, c.w, c.offsets, activation=act)
+    m = c.member()
+    inside = check_range(torch, got_dx[m], dx[m], rounded(torch, dx, dx_off, t)[m], t, "dx")
+    inside_dw = check_range(torch, got_dw, dw, rounded(torch, dw, dw_off, t), t, "dw")
+    if size < 2000:  # nothing is infinite here
+        assert inside.all() and inside_dw.all() and got_dx[m].isfinite().all() and got_dw.isfinite().all()
+    none, wide = moe.gated_product_backward(dh, gu, c.x, c.w, c.offsets, activation=act, need_dx=False, dw_dtype=torch.float32)
+    check(torch, wide, dw, rounded(torch, dw, dw_off, torch.float32), "dw fp32")
+    # the other groups' results are those of a call in which nothing is far out
+    dh[rows] /= size
+    gu[rows, n:] /= size
+    near_dx, near_dw = moe.gated_product_backward(dh, gu, c.x, c.w, c.offsets, activation=act)
+    assert torch.equal(near_dx[sizes[0]:c.ends[-1]], got_dx[sizes[0]:c.ends[-1]]) and torch.equal(near_dw[1:], got_dw[1:])
+
+
+def test_gated_backward_past_65504_beside_infinities(torch, moe):
+    """An infinite dh is not a large one: its row and its columns of dw are not finite, the others are right."""
+    t, n, k = torch.float16, 72, 136
+    c = Case(torch, [40, 30], n, k, t, wide=2)
+    dh, gu = far_out(torch, c, n, torch.tensor([3, 50], device="cuda"), 300.0)
+    dh[5, 7] = float("inf")
+    dh[51, 2] = float("nan")
+    dx, dw = moe.gated_product_backward(dh, gu, c.x, c.w, c.offsets)
+    rest = torch.ones(70, dtype=torch.bool, device="cuda")
+    rest[[5, 51]] = False
+    assert dx[rest].isfinite().all() and not dx[5].isfinite().any() and dx[51].isnan().all()
+    cols = torch.ones(2, 2 * n, dtype=torch.bool, device="cuda")
+    cols[0, [7, n + 7]] = False
+    cols[1, [2, n + 2]] = False
+    assert dw[cols].isfinite().all() and not dw[~cols].isfinite().any()
+    clean = dh.clone()
+    clean[5, 7], clean[51, 2] = 0, 0
+    d, off = slopes64(torch, "silu", clean, gu, n, t)
+    off = off + 2.0 ** -25 * lifts(torch, c, d, t)
+    rx, rw, rx_off, rw_off = grads64(torch, c, d, off)
+    check(torch, dx[rest], rx[rest], rounded(torch, rx, rx_off, t)[rest], "dx")
+    check(torch, dw[cols], rw[cols], rounded(torch, rw, rw_off, t)[cols], "dw")
+
+
+def test_gated_backward_past_65504_replays(torch, moe):
+    """A captured call scales where the inputs of a replay ask for it, and not on the next."""
+    t, n, k = torch.float16, 264, 136
+    c = Case(torch, [40, 300], n, k, t, wide=2)
+    near = (c.normal(340, n), c.normal(340, 2 * n))
+    c.x.mul_(2.0 ** -8)
+    c.w.mul_(2.0 ** -8)
+    dh, gu = (a.clone() for a in near)
+    ws = sentinel(torch, moe.product_workspace("gated_product_backward", 340, n, k, 2, dtype=t))
+    moe.gated_product_backward(dh, gu, c.x, c.w, c.offsets, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = moe.gated_product_backward(dh, gu, c.x, c.w, c.offsets, workspace=ws)
+    for rows in ([], [5], [100, 7], [], [200]):
+        dh.copy_(near[0])
+        gu.copy_(near[1])
+        dh[rows] *= 300.0
+        gu[rows, n:] *= 300.0
+        ws.fill_(0xFF)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = moe.gated_product_backward(dh, gu, c.x, c.w, c.offsets)
+        torch.cuda.synchronize()
+        for a, b in zip(out, eager):
+            assert a.isfinite().all() and torch.equal(a, b), rows
+    del graph

@@ -194,3 +194,14 @@ def test_binding_refuses_what_the_library_cannot_see():
     with pytest.raises(moe.MoeError) as e:
         moe.product_workspace("expert_product", 1, 12, 8)
     assert e.value.status == SHAPE
+
+
+def test_workspace_holds_the_groups_largest_slopes(lib):
+    """fp16 only: one word a group behind (dg, du); nothing without rows, where the call takes no workspace."""
+    kw = dict(rows=1000, n=64, k=64, groups=200)
+    plain, lifted = (workspace(lib, "gated_product_backward", type=t, **kw)[1] for t in (BF16, FP16))
+    assert lifted >= plain + 4 * 200
+    assert workspace(lib, "expert_product_backward", type=FP16, **kw) == workspace(lib, "expert_product_backward", **kw)
+    for t in (BF16, FP16):
+        assert workspace(lib, "gated_product_backward", rows=0, groups=200, type=t) == (0, 0)
+        assert backward(lib, True, type=t, ws=None, ws_bytes=0) == 0
