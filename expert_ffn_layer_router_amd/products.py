@@ -48,9 +48,17 @@ def _env():
     return _Torch()
 
 
+def _fits(**sizes):
+    """Refuses sizes that the C interface's int32 would cut to their low bits."""
+    for name, size in sizes.items():
+        if not -(1 << 31) <= size < 1 << 31:
+            raise _lib.MoeError(_lib.MOE_ERR_UNSUPPORTED_SHAPE, f"{name}={size} is out of range")
+
+
 @lru_cache(maxsize=1024)
 def _shape(op: int, rows: int, n: int, k: int, groups: int, type_: int, act: int):
     """(the C struct, workspace bytes) of a call: pure host arithmetic of its arguments."""
+    _fits(rows=rows, n=n, k=k, groups=groups)
     p = _lib.MoeProduct(rows, n, k, groups, type_, act)
     need = ctypes.c_size_t()
     _lib.check(_lib.load().moe_product_workspace(ctypes.byref(p), op, ctypes.byref(need)))
@@ -198,6 +206,8 @@ def quantize_rows(x, codes=None, scale=None, stream=None):
     scale = max|row| / 127, codes = rint(row / scale) (moe_quantize_rows)."""
     rows = _matrix_rows("x", x)
     k = x.shape[1]
+    if rows | k > 0x7FFFFFFF:
+        _fits(rows=rows, k=k)
     with _Call(x, stream) as c:
         px, ldx = c.rows("x", x, rows, k, x.dtype)
         codes, pc, ldc = c.result("codes", codes, rows, k, c.env.int8)

@@ -205,3 +205,20 @@ def test_workspace_holds_the_groups_largest_slopes(lib):
     for t in (BF16, FP16):
         assert workspace(lib, "gated_product_backward", rows=0, groups=200, type=t) == (0, 0)
         assert backward(lib, True, type=t, ws=None, ws_bytes=0) == 0
+
+
+def test_sizes_past_32_bits_are_refused():
+    """A size that does not fit the C struct's int32 is refused, not cut to its low bits."""
+    import torch
+
+    import expert_ffn_layer_router_amd as moe
+    good = dict(rows=1000, n=256, k=8192, groups=1)
+    for name in good:
+        for size in (1 << 31, (1 << 32) + good[name], (1 << 40) + good[name], -(1 << 32) + good[name]):
+            with pytest.raises(moe.MoeError, match=name) as e:
+                moe.product_workspace("expert_product", **{**good, name: size})
+            assert e.value.status == SHAPE
+    for name, shape in (("rows", ((1 << 32) + 4, 64)), ("k", (4, (1 << 32) + 64))):
+        with pytest.raises(moe.MoeError, match=name) as e:  # refused before the device is looked at
+            moe.quantize_rows(torch.empty(1, dtype=torch.bfloat16).expand(shape))
+        assert e.value.status == SHAPE
