@@ -292,13 +292,26 @@ def gated_product(x, w, offsets=None, activation="silu", save=False, out=None, g
 def _backward(name, dy, gate_up, x, w, offsets, activation, need_dx, need_dw, dx, dw, dw_dtype, workspace, stream):
     gated = activation is not None
     rows = _matrix_rows("dh" if gated else "dy", dy)
-    groups, n, k = _weights(w, gated)
     dtype = dy.dtype
     need_dx, need_dw = need_dx or dx is not None, need_dw or dw is not None
+    if x is None and need_dw:
+        raise ValueError("x is needed for dw")
+    if w is not None:
+        groups, n, k = _weights(w, gated)
+        w_shape = w.shape
+    else:
+        if need_dx or x is None:
+            raise ValueError("w is needed for dx" if need_dx else "x or w is needed")
+        _matrix_rows("x", x)
+        n, k = dy.shape[1], x.shape[1]
+        groups = 1 if offsets is None else offsets.numel() - 1
+        w_shape = (groups, 2 * n if gated else n, k)
+        if offsets is None and (dw is None or dw.dim() == 2):
+            w_shape = w_shape[1:]
     with _Call(dy, stream) as c:
         py, ldy = c.rows("dh" if gated else "dy", dy, rows, n, dtype)
-        px, ldx = c.rows("x", x, rows, k, dtype)
-        pw = c.plain("w", w, w.shape, dtype)
+        px, ldx = (None, 0) if x is None else c.rows("x", x, rows, k, dtype)
+        pw = None if w is None else c.plain("w", w, w_shape, dtype)
         po = c.offsets(offsets, groups)
         shape, need = _shape(_lib.MOE_OPS[name], rows, n, k, groups, _type(dtype), _act(activation) if gated else 0)
         pdx, lddx, pdw = None, 0, None
@@ -306,8 +319,8 @@ def _backward(name, dy, gate_up, x, w, offsets, activation, need_dx, need_dw, dx
             dx, pdx, lddx = c.result("dx", dx, rows, k, dtype)
         if need_dw:
             if dw is None:
-                dw = c.empty(w.shape, dw_dtype or dtype)
-            pdw = c.plain("dw", dw, w.shape, dw_dtype or dw.dtype)
+                dw = c.empty(w_shape, dw_dtype or dtype)
+            pdw = c.plain("dw", dw, w_shape, dw_dtype or dw.dtype)
         ws, ws_bytes, _alive = c.workspace(workspace, need)
         dw_type = _type(dw.dtype) if need_dw else shape.type
         head = (ctypes.byref(shape), py, ldy)
@@ -323,13 +336,15 @@ def _backward(name, dy, gate_up, x, w, offsets, activation, need_dx, need_dw, dx
 def expert_product_backward(dy, x, w, offsets=None, need_dx=True, need_dw=True, dx=None, dw=None, dw_dtype=None,
                             workspace=None, stream=None):
     """(dx, dw) of expert_product for the gradient dy [rows, n]: dx = dy w[e], dw[e] = dy_e^T x_e (of w's
-    dtype, or `dw_dtype` fp32; zero for a group without rows).  What is not needed is None."""
+    dtype, or `dw_dtype` fp32; zero for a group without rows).  What is not needed is None.  x may be None
+    without dw, w without dx (dw is then [groups, n, k], or [n, k] without offsets)."""
     return _backward("expert_product_backward", dy, None, x, w, offsets, None, need_dx, need_dw, dx, dw, dw_dtype,
                      workspace, stream)
 
 
 def gated_product_backward(dh, gate_up, x, w, offsets=None, activation="silu", need_dx=True, need_dw=True, dx=None,
                            dw=None, dw_dtype=None, workspace=None, stream=None):
-    """(dx, dw) of gated_product for the gradient dh [rows, n] and the gate_up it saved."""
+    """(dx, dw) of gated_product for the gradient dh [rows, n] and the gate_up it saved; the rest as for
+    expert_product_backward."""
     return _backward("gated_product_backward", dh, gate_up, x, w, offsets, activation or "silu", need_dx, need_dw, dx,
                      dw, dw_dtype, workspace, stream)

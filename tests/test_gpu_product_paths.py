@@ -457,3 +457,35 @@ def test_gated_backward_past_65504_replays(torch, moe):
         for a, b in zip(out, eager):
             assert a.isfinite().all() and torch.equal(a, b), rows
     del graph
+
+
+# ---- gradients of one side only ------------------------------------------------------------
+
+@pytest.mark.parametrize("sizes", [[40, 0, 17], [57]], ids=str)
+def test_backward_without_the_other_operand(torch, moe, sizes):
+    """dx needs no x, dw needs no w: the results are those of the call that has both."""
+    n, k, bf16 = 72, 136, torch.bfloat16
+    for wide in (1, 2):
+        c = Case(torch, sizes, n, k, bf16, wide=wide, offsets=len(sizes) > 1)
+        w = c.w if len(sizes) > 1 else c.w[0]
+        dy, gu = c.normal(c.rows, n), c.normal(c.rows, 2 * n)
+
+        def call(x, w, **kw):
+            if wide == 2:
+                return moe.gated_product_backward(dy, gu, x, w, c.offsets, **kw)
+            return moe.expert_product_backward(dy, x, w, c.offsets, **kw)
+
+        dx, dw = call(c.x, w)
+        only, none = call(None, w, need_dw=False)
+        assert none is None and torch.equal(only, dx)
+        none, only = call(c.x, None, need_dx=False)
+        assert none is None and only.shape == dw.shape and torch.equal(only, dw)
+        given = torch.empty(dw.shape, dtype=torch.float32, device="cuda")
+        _, only = call(c.x, None, need_dx=False, dw=given)
+        assert only is given and torch.equal(only.to(bf16), dw)
+        with pytest.raises(ValueError, match="x is needed"):
+            call(None, w)
+        with pytest.raises(ValueError, match="w is needed"):
+            call(c.x, None)
+        with pytest.raises(ValueError, match="dw must be"):
+            call(c.x, None, need_dx=False, dw=given[..., :8].contiguous())

@@ -222,3 +222,26 @@ def test_sizes_past_32_bits_are_refused():
         with pytest.raises(moe.MoeError, match=name) as e:  # refused before the device is looked at
             moe.quantize_rows(torch.empty(1, dtype=torch.bfloat16).expand(shape))
         assert e.value.status == SHAPE
+
+
+def test_binding_names_the_operand_that_a_gradient_needs():
+    import torch
+
+    import expert_ffn_layer_router_amd as moe
+    x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(1, 48, 64, dtype=torch.bfloat16)
+    dy, dh = torch.zeros(4, 48, dtype=torch.bfloat16), torch.zeros(4, 24, dtype=torch.bfloat16)
+    for call in (lambda x, w, **kw: moe.expert_product_backward(dy, x, w, **kw),
+                 lambda x, w, **kw: moe.gated_product_backward(dh, dy, x, w, **kw)):
+        with pytest.raises(ValueError, match="x is needed for dw"):
+            call(None, w)
+        with pytest.raises(ValueError, match="x is needed for dw"):
+            call(None, w, need_dw=False, dw=w)  # a dw to fill asks for it
+        with pytest.raises(ValueError, match="w is needed for dx"):
+            call(x, None)
+        with pytest.raises(ValueError, match="x or w is needed"):
+            call(None, None, need_dx=False, need_dw=False)
+        for one in (lambda: call(None, w, need_dw=False), lambda: call(x, None, need_dx=False)):
+            with pytest.raises(ValueError, match="GPU"):  # as far as a host tensor comes
+                one()
+        with pytest.raises(ValueError, match="matrix"):
+            call(x[0], None, need_dx=False)
