@@ -14,7 +14,8 @@ a product's codes); weights, scales and offsets are contiguous.  A call runs on 
 not given there; with `out` and `workspace` given it allocates nothing.  On
 another stream than the current one the caller orders the call after what
 wrote its inputs; their memory is kept from reuse until it is done.  Nothing is
-recorded for autograd: the backward calls are the caller's."""
+recorded for autograd: the backward calls are the caller's, and with gradients
+enabled a tensor that requires one is refused (its result would be cut off)."""
 
 from __future__ import annotations
 
@@ -37,6 +38,7 @@ class _Torch:
         self.types = {torch.bfloat16: _lib.MOE_TYPE_BF16, torch.float16: _lib.MOE_TYPE_FP16,
                       torch.float32: _lib.MOE_TYPE_FP32}
         self.current_device = torch.cuda.current_device
+        self.grad_enabled = torch.is_grad_enabled
         # the raw handle without a Stream object around it (2 us less), where this torch has it
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                                   lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -133,6 +135,8 @@ class _Call:
         """(pointer, row stride) of a [rows, width] matrix."""
         if t.shape != (rows, width) or t.dtype is not dtype or t.get_device() != self.index:
             self.refuse(name, t, (rows, width), dtype)
+        if t.requires_grad and self.env.grad_enabled():
+            self.refuse_tracked(name)
         stride, one = t.stride()
         if one != 1:
             raise ValueError(f"the values of a row of {name} must be contiguous")
@@ -144,6 +148,8 @@ class _Call:
         """Pointer of a contiguous tensor."""
         if t.shape != shape or t.dtype is not dtype or t.get_device() != self.index:
             self.refuse(name, t, shape, dtype)
+        if t.requires_grad and self.env.grad_enabled():
+            self.refuse_tracked(name)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         if self.other is not None:
@@ -156,6 +162,10 @@ class _Call:
         if t.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+
+    def refuse_tracked(self, name):
+        raise ValueError(f"{name} requires a gradient, and this call records nothing for autograd: call it under "
+                         "torch.no_grad() or from a torch.autograd.Function, and its backward call there")
 
     def offsets(self, offsets, groups):
         if offsets is None:

@@ -489,3 +489,30 @@ def test_backward_without_the_other_operand(torch, moe, sizes):
             call(c.x, None)
         with pytest.raises(ValueError, match="dw must be"):
             call(c.x, None, need_dx=False, dw=given[..., :8].contiguous())
+
+
+# ---- autograd ---------------------------------------------------------------------------------
+
+def test_tensors_that_autograd_tracks_are_refused(torch, moe):
+    """No call records anything for autograd, so one that autograd expects a gradient from is refused: a result cut
+    off without a word would train nothing."""
+    bf16 = torch.bfloat16
+    x, w = torch.randn(4, 64, device="cuda").to(bf16), torch.randn(1, 48, 64, device="cuda").to(bf16)
+    dy, gu = torch.randn(4, 24, device="cuda").to(bf16), torch.randn(4, 48, device="cuda").to(bf16)
+    codes, scale = moe.quantize_rows(x)
+    wq, ws = torch.ones(1, 48, 64, dtype=torch.int8, device="cuda"), torch.ones(1, 48, device="cuda")
+    every = [(moe.quantize_rows, (x,)), (moe.expert_product, (x, w)), (moe.gated_product, (x, w)),
+             (moe.int8_product, (codes, scale, wq, ws)), (moe.int8_gated, (codes, scale, wq, ws)),
+             (moe.gated_product_backward, (dy, gu, x, w)), (moe.expert_product_backward, (gu, x, w))]
+    for fn, args in every:
+        ref = tensors(fn(*args))
+        for i, a in enumerate(args):
+            if not a.is_floating_point():
+                continue
+            leaf = list(args)
+            leaf[i] = a.detach().clone().requires_grad_()
+            with pytest.raises(ValueError, match="autograd"):
+                fn(*leaf)
+            with torch.no_grad():
+                for b, c in zip(tensors(fn(*leaf)), ref):
+                    assert torch.equal(b, c) and not b.requires_grad

@@ -245,3 +245,22 @@ def test_binding_names_the_operand_that_a_gradient_needs():
                 one()
         with pytest.raises(ValueError, match="matrix"):
             call(x[0], None, need_dx=False)
+
+
+def test_binding_refuses_what_autograd_tracks():
+    """The checks of one call on the tensors themselves (a host tensor stands for the device's)."""
+    import torch
+
+    from expert_ffn_layer_router_amd import products
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, requires_grad=True)
+    call = object.__new__(products._Call)
+    call.env, call.index, call.other, call.like = products._env(), x.get_device(), None, x
+    for tracked in (x, x * 2):  # a leaf and a result
+        with pytest.raises(ValueError, match="x requires a gradient.*autograd"):
+            call.rows("x", tracked, 4, 64, torch.bfloat16)
+        with pytest.raises(ValueError, match="w requires a gradient.*autograd"):
+            call.plain("w", tracked, (4, 64), torch.bfloat16)
+        with torch.no_grad():
+            assert call.rows("x", tracked, 4, 64, torch.bfloat16) == (tracked.data_ptr(), 64)
+            assert call.plain("w", tracked, (4, 64), torch.bfloat16) == tracked.data_ptr()
+    assert call.rows("x", x.detach(), 4, 64, torch.bfloat16) == (x.data_ptr(), 64)
