@@ -13,7 +13,7 @@ inside the bound there, 2e (8 + 4 |z|) = 16 e, 24 e, 32 e, ..."""
 import pytest
 
 from gpu_util import say
-from test_gpu_products import (E, TYPES, Case, check, gated64, grads64, int_case, rounded, slopes64,
+from test_gpu_products import (E, TYPES, Case, check, gated64, grads64, half_step, int_case, rounded, slopes64,
                                tensors)
 from test_gpu_products import moe, torch  # noqa: F401  (fixtures)
 
@@ -516,3 +516,26 @@ def test_tensors_that_autograd_tracks_are_refused(torch, moe):
             with torch.no_grad():
                 for b, c in zip(tensors(fn(*leaf)), ref):
                     assert torch.equal(b, c) and not b.requires_grad
+
+
+# ---- subnormal operands and results -------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("sizes,n,k", [([9, 0, 3], 72, 136), ([700, 0, 900], 1544, 144), ([5000, 1, 333], 1032, 144)], ids=str)
+def test_subnormal_values(torch, moe, sizes, n, k, dtype):
+    """Operands below the type's normal range count in full, and results there are rounded to its subnormals."""
+    t = getattr(torch, dtype)
+    tiny = torch.finfo(t).smallest_normal
+    half_subnormal = tiny * torch.finfo(t).eps / 2
+    c = Case(torch, sizes, n, k, t)
+    # bf16 shares fp32's exponents: there the other operand lifts the results to about 2^-122, and one below the
+    # normal range (2^-126) may be flushed
+    c.x = (c.x.double() * tiny / 4).to(t)
+    c.w = (c.w.double() * (1 if t == torch.float16 else 64)).to(t)
+    y, before = c.forward()
+    bound = before + half_step(torch, t) * (y.abs() + before) + half_subnormal + 2.0 ** -126 * (t == torch.bfloat16)
+    check(torch, moe.expert_product(c.x, c.w, c.offsets), y, bound, "y")
+    dy = (c.normal(c.rows, n).double() * tiny / 8).to(t)
+    dx, _, dx_off, _ = grads64(torch, c, dy.double(), torch.zeros(c.rows, n, dtype=torch.float64, device="cuda"))
+    bound = dx_off + half_step(torch, t) * (dx.abs() + dx_off) + half_subnormal + 2.0 ** -126 * (t == torch.bfloat16)
+    check(torch, moe.expert_product_backward(dy, c.x, c.w, c.offsets, need_dw=False)[0], dx, bound, "dx")
