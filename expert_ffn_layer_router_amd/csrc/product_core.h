@@ -36,10 +36,12 @@ __device__ __forceinline__ float half_to_f32(bool fp16, uint16_t b) { return fp1
 // With t = exp(-|z|) and r = 1 / (1 + t), s is r or t r by the sign of z and
 // 1 - s the other, so neither overflows nor cancels.  The hardware exp2 and
 // reciprocal flush subnormal results: t is carried as t 2^64, so that act(g)
-// keeps its precision as far down as fp32 goes.
+// goes as far down as fp32 does.  Adding 64 rounds exp2's argument to 2^-19 for
+// |z| < 22: t is off by up to 2^-19 ln 2 = 1.3e-6 of itself, act(g) by 1 - s
+// times that, 370 times less than the half step of an fp16 result.
 constexpr float kGeluC2 = 1.5957691216057308f;  // 2 sqrt(2/pi)
 constexpr float kGeluB = 0.044715f;
-constexpr float kLift = 0x1p64f, kDrop = 0x1p-64f;
+constexpr float kDrop = 0x1p-64f;
 struct Gate {
   float z, dz, r, low;  // low = t r 2^64
 };

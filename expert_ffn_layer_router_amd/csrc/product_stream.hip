@@ -21,7 +21,9 @@
 // 128-byte lines (eight lanes a row, two more moves a fragment) gained 6% where
 // memory is the bound (16 x 12800 of 4096: 25.1 against 26.6) and lost 10-25%
 // elsewhere; 8 waves a block: 28.3 -> 29.5 at 16 x 4096 of 14336, 16 x 8192 of
-// 4096: 17.0 -> 19.0.
+// 4096: 17.0 -> 19.0.  The exchange itself costs where rows are short and groups
+// many: 96 rows over 64 groups of 4096 columns of 2048 codes 50.6 -> 54.5 us,
+// the one shape of those timed that lost by it.
 //
 // 32 rows over 8 groups of 14336 gated columns of 4096 codes: 160 us, 5.9 TB/s
 // (a read-only stream reaches 6.7); 16 rows x one group of 6400 gated columns

@@ -34,7 +34,8 @@
  *     Offsets out of order or out of range give unspecified rows but no
  *     access outside the matrices.
  *   - Sums run over fp32 (16-bit operands) or int32 (codes, exact) and are
- *     rounded once to the output's type.  The same call gives the same bits.
+ *     rounded once to the output's type.  Codes: (sum * scale) * w_scale, each
+ *     product in fp32, so that sum * scale has to stay in its range too.  The same call gives the same bits.
  *   - A workspace needs no initialisation and keeps nothing between calls;
  *     calls that share one (captured graphs among them) must not overlap in
  *     time.  It may be NULL where moe_product_workspace says 0.
