@@ -204,10 +204,11 @@ Result forward_result(const moe_product* p, bool gated) {
   return gated ? Result::kGated : p->type == MOE_TYPE_FP32 ? Result::kWide : Result::kHalf;
 }
 
-// The gated backward pass's (dg, du), and in fp16 each group's largest behind them.
+// The gated backward pass's (dg, du), and each group's largest behind them (used in
+// fp16; reserved in both types, so that one workspace serves either).
 size_t slopes_only_bytes(const moe_product* p) { return align_up((size_t)p->rows * 2 * p->n * 2); }
 size_t slopes_bytes(const moe_product* p) {
-  return slopes_only_bytes(p) + (p->type == MOE_TYPE_FP16 && p->rows > 0 ? align_up(p->groups * sizeof(uint32_t)) : 0);
+  return slopes_only_bytes(p) + (p->rows > 0 ? align_up(p->groups * sizeof(uint32_t)) : 0);
 }
 
 size_t workspace_bytes_of(const moe_product* p, moe_op op) {

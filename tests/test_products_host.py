@@ -197,14 +197,21 @@ def test_binding_refuses_what_the_library_cannot_see():
 
 
 def test_workspace_holds_the_groups_largest_slopes(lib):
-    """fp16 only: one word a group behind (dg, du); nothing without rows, where the call takes no workspace."""
+    """One word a group behind (dg, du); nothing without rows, where the call takes no workspace."""
     kw = dict(rows=1000, n=64, k=64, groups=200)
-    plain, lifted = (workspace(lib, "gated_product_backward", type=t, **kw)[1] for t in (BF16, FP16))
-    assert lifted >= plain + 4 * 200
-    assert workspace(lib, "expert_product_backward", type=FP16, **kw) == workspace(lib, "expert_product_backward", **kw)
+    dgu = 1000 * 2 * 64 * 2
     for t in (BF16, FP16):
+        gated, plain = (workspace(lib, f"{op}_backward", type=t, **kw)[1] for op in ("gated_product", "expert_product"))
+        assert plain == 0 and gated >= dgu + 4 * 200
         assert workspace(lib, "gated_product_backward", rows=0, groups=200, type=t) == (0, 0)
         assert backward(lib, True, type=t, ws=None, ws_bytes=0) == 0
+
+
+@pytest.mark.parametrize("op", sorted(_lib.MOE_OPS))
+def test_workspace_does_not_depend_on_the_16_bit_type(lib, op):
+    """A workspace sized without naming the type (bf16) serves the same shape in fp16."""
+    for kw in (dict(rows=1000, n=256, k=8192), dict(rows=77, n=64, k=64, groups=256), dict(rows=0), dict(rows=5000, n=4096, k=4096)):
+        assert workspace(lib, op, type=BF16, **kw) == workspace(lib, op, type=FP16, **kw)
 
 
 def test_sizes_past_32_bits_are_refused():
