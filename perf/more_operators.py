@@ -107,8 +107,6 @@ def draw(rng):
             case["act"] = rng.choice(["silu", "gelu"])
         if op == "gated":
             case["save"] = rng.random() < 0.5
-        if op == "product":
-            case["type"] = rng.choice(["bf16", "fp16", "fp32"])
         weights = case["groups"] * case["n"] * case["k"] * (2 if "gated" in op else 1)
         if work(case)["flops"] <= MOST_FLOPS and weights <= MOST_WEIGHTS:
             return case
