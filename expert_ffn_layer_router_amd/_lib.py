@@ -25,6 +25,7 @@ MOE_TYPE_BF16, MOE_TYPE_FP16, MOE_TYPE_FP32 = 0, 1, 2
 MOE_ACT_SILU, MOE_ACT_GELU = 0, 1
 MOE_OPS = {"int8_product": 0, "int8_gated": 1, "expert_product": 2, "expert_product_backward": 3,
            "gated_product": 4, "gated_product_backward": 5}
+MOE_FP8_OPS = {"fp8_product": 0, "fp8_gated": 1, "fp8_product_backward": 2, "fp8_gated_backward": 3}
 
 
 class MoeConfig(ctypes.Structure):
@@ -46,6 +47,17 @@ class MoeRouting(ctypes.Structure):
 
 class MoeProduct(ctypes.Structure):
     _fields_ = [(name, ctypes.c_int32) for name in ("rows", "n", "k", "groups", "type", "activation")]
+
+
+class MoeAdamw(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_double) for name in ("lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")] + [
+        ("seed", ctypes.c_uint64), ("step", ctypes.c_int32), ("state_bits", ctypes.c_int32)] + [
+        (name, ctypes.c_void_p) for name in ("device_lr", "device_grad_scale", "device_step")]
+
+
+class MoeAdamwTensor(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("param", "grad", "master", "m", "v", "m_scale", "v_scale")] + [
+        ("count", ctypes.c_int64), ("param_type", ctypes.c_int32), ("grad_type", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -112,6 +124,14 @@ def load():
         "moe_gated_product": (c_int, [product, vp, i64, vp, vp, vp, i64, vp, i64, vp, sz, vp]),
         "moe_gated_product_backward": (c_int, [product, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i32, vp, sz,
                                                vp]),
+        "moe_fp8_workspace": (c_int, [product, c_int, ctypes.POINTER(sz)]),
+        "moe_quantize_blocks": (c_int, [i32, i32, i32, vp, i64, vp, i64, vp, i64, vp]),
+        "moe_quantize_tiles": (c_int, [i32, i32, i32, i32, vp, vp, vp, vp]),
+        "moe_fp8_product": (c_int, [product, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, sz, vp]),
+        "moe_fp8_gated": (c_int, [product, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, sz, vp]),
+        "moe_fp8_product_backward": (c_int, [product, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, sz, vp]),
+        "moe_fp8_gated_backward": (c_int, [product, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, sz, vp]),
+        "moe_adamw_step": (c_int, [ctypes.POINTER(MoeAdamw), i32, ctypes.POINTER(MoeAdamwTensor), vp]),
         "moe_status_string": (ctypes.c_char_p, [c_int]),
         "moe_last_error": (ctypes.c_char_p, []),
     }

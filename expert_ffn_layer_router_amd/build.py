@@ -23,7 +23,8 @@ LIB_NAME = "libmoe_hip.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["router.hip", "permute.hip", "stream_gemm.hip", "prefill_gemm.hip", "combine.hip", "moe_api.hip",
            "expert_cache.hip", "measure.hip", "ops_api.hip", "product_int8.hip", "product_half.hip", "product_grad.hip",
-           "product_stream.hip", "product_rows.hip"]
+           "product_stream.hip", "product_rows.hip", "fp8_api.hip", "fp8_tile.hip", "fp8_stream.hip", "fp8_rows.hip",
+           "adamw.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
