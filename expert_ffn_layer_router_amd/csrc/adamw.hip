@@ -130,7 +130,7 @@ __device__ __forceinline__ u32x2 code8(const float* x, const uint32_t* u, float&
   for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
   top = max16(top);
   const bool finite = top < 0x7F800000u;
-  scale = finite ? __uint_as_float(top) / F::kMost : __uint_as_float(0x7FC00000u);
+  scale = finite ? __uint_as_float(top) * (1.0f / F::kMost) : __uint_as_float(0x7FC00000u);
   const bool some = finite && scale > 0.0f;
   const int se = some ? __builtin_amdgcn_frexp_expf(scale) : 0;
   const float sn = some ? __builtin_amdgcn_ldexpf(scale, -se) : 1.0f;

@@ -138,7 +138,7 @@ class _Call:
         if t.requires_grad and self.env.grad_enabled():
             self.refuse_tracked(name)
         stride, one = t.stride()
-        if one != 1:
+        if one != 1 and width != 1:
             raise ValueError(f"the values of a row of {name} must be contiguous")
         if self.other is not None:
             t.record_stream(self.other)

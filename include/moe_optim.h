@@ -9,8 +9,8 @@
  *        - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
  *
  * in fp32.  The states m and v are kept in fp32, or in 8 bits with an fp32
- * scale for each 128 consecutive values: m as e4m3 (a scale of max |m| / 448),
- * v as e5m2 (max v / 57344).  An 8-bit state rounds to one of its two
+ * scale for each 128 consecutive values: m as e4m3 (its scale is max |m| times
+ * the fp32 nearest 1 / 448), v as e5m2 (max v times that nearest 1 / 57344).  An 8-bit state rounds to one of its two
  * neighbouring codes at random, up with the probability that keeps its mean,
  * because a step moves v by a thousandth and a code by an eighth: rounded to
  * the nearest, v would stand still.  v above 0 never becomes a code of 0

@@ -63,7 +63,7 @@ def coded(x, u, most, lowest, bits):
     rand[:x.size] = u.astype(F32) / F32(65536)
     whole, rand = whole.reshape(blocks, 128), rand.reshape(blocks, 128)
     top = np.abs(whole).max(1, keepdims=True)
-    scale = top / F32(most)
+    scale = top * (F32(1) / F32(most))
     y = np.abs(whole) / np.where(scale > 0, scale, F32(1))
     unit = np.maximum(np.frexp(y)[1] - 1, lowest) - bits
     n = np.floor(np.ldexp(y, -unit) + rand)
