@@ -20,7 +20,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
   constexpr bool GATED = RES == Result::kGated;
   constexpr int BK = kScaleBlock;  // contraction values, and bytes of a row, per stage
   constexpr int kPBytes = BM * BK, kQBytes = BN * BK;
-  constexpr int kSlot = kPBytes + kQBytes;
+  constexpr int kSlot = kPBytes;  // ring slot: one operand's stage
   constexpr int PI = kPBytes / 1024 / NW, QI = kQBytes / 1024 / NW;  // 1 KB copies per wave and stage
   constexpr int NO = GATED ? BN / 2 : BN;                            // result columns per block
   constexpr int NS = GATED ? 2 : 1;                                  // column scales of a wave
@@ -28,8 +28,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
   static_assert(!GATED || NJ % 2 == 0, "gate and up tiles in pairs");
   static_assert(NO % (16 * NJ / NS) == 0 && kScaleBlock % (16 * NJ / NS) == 0 && (!GATED || kScaleBlock % NO == 0),
                 "a wave's columns share a scale");
-  static_assert(BM * BN * 2 <= 2 * kSlot, "the 16-bit result fits the stages' LDS");
-  __shared__ __attribute__((aligned(1024))) char smem_raw[2 * kSlot];
+  static_assert(PI == QI && BM * BN * 2 <= kRing * kSlot, "equal slots; the 16-bit result fits the ring");
+  constexpr int R = 4;         // P fragments in registers
+  constexpr int kTurn = MI - 2;  // row blocks before the turn
+  constexpr int kPCopies = (PI + kTurn - 1) / kTurn;  // P copies of a row block before it
+  static_assert(MI >= R && NJ == 4 && PI == 4, "the rows' schedule");
+  __shared__ __attribute__((aligned(1024))) char smem_raw[kRing * kSlot];
   lds_char* smem = (lds_char*)smem_raw;
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -67,121 +71,216 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
     const char* pbase = a.p + (int64_t)row0 * a.ldp;
     const char* qbase = a.q + (int64_t)t.group * a.q_group + (Q_STR ? (int64_t)n0 : (int64_t)n0 * a.ldq);
     uint32_t pv[PI], qv[QI];  // byte offsets of this lane's copies, or kNoLoad
-    int pk[PI], qk[QI];       // their contraction position in the stage
+    // where this lane's c-th copy lies in the stage's contraction: contiguous
+    // operands (LDS row r holds chunk c of 16 bytes at c ^ (r / 2) % 8), strided
+    const int chunk0 = 16 * ((lane & 7) ^ (lane >> 4));
+    auto chunk_at = [&](int c) { return chunk0 ^ (c & 1) * 64; };
+    constexpr int cpr = BN / 16;  // strided: 16-byte chunks per LDS row
+    auto q_at = [&](int c) { return (wave * QI + c) * (64 / cpr) + lane / cpr; };
+    static_assert(PI % 2 == 0, "a wave's copies begin at a multiple of 16 rows");
 #pragma unroll
     for (int c = 0; c < PI; ++c) {
-      const int r = (wave * PI + c) * 8 + lane / 8, chunk = (lane & 7) ^ ((r >> 1) & 7);
-      pv[c] = r < live ? (uint32_t)(r * a.ldp + 16 * chunk) : kNoLoad;
-      pk[c] = 16 * chunk;
+      const int r = (wave * PI + c) * 8 + lane / 8;
+      pv[c] = r < live ? (uint32_t)(r * a.ldp + chunk_at(c)) : kNoLoad;
     }
 #pragma unroll
     for (int c = 0; c < QI; ++c) {
       if constexpr (Q_STR) {
-        constexpr int cpr = BN / 16;  // 16-byte chunks per LDS row
-        const int kr = (wave * QI + c) * (64 / cpr) + lane / cpr;
+        const int kr = q_at(c);
         const int fold = cpr == 16 ? (kr & 7) | (kr >> 1 & 8) : (kr >> 1 & 3) | (kr >> 2 & 4);
         const int chunk = (lane % cpr) ^ fold;
         qv[c] = n0 + 16 * chunk < ncols ? (uint32_t)(kr * a.ldq + 16 * chunk) : kNoLoad;
-        qk[c] = kr;
       } else {
-        const int r = (wave * QI + c) * 8 + lane / 8, chunk = (lane & 7) ^ ((r >> 1) & 7);
+        const int r = (wave * QI + c) * 8 + lane / 8;
         int src = r;
         if constexpr (GATED) {  // LDS row r: tile r / 16 belongs to wave column (r / 16) / NJ
           const int jb = r / 16;
           src = (jb / NJ * (NJ / 2) + jb % NJ / 2) * 16 + r % 16;
         }
-        qv[c] = n0 + src < ncols ? (uint32_t)(src * a.ldq + 16 * chunk) : kNoLoad;
-        qk[c] = 16 * chunk;
+        qv[c] = n0 + src < ncols ? (uint32_t)(src * a.ldq + chunk_at(c)) : kNoLoad;
       }
     }
-    auto copy_stage = [&](int slot, int st) {
-      const int half = st >= half_stages ? 1 : 0, in = st - half * half_stages;
-      const int left = a.contract - in * BK;
-      lds_char* dst = smem + slot * kSlot;
-      const __amdgpu_buffer_rsrc_t pr = buffer_at(pbase + (int64_t)st * BK);
+    // The copies of an operand's stage: begin_p / begin_q set the descriptor
+    // (and, in the contraction's last stage and past it, drop the lanes with
+    // nothing to load: in place, so that the copies' offsets live in registers
+    // of their own, and without a branch, behind which the compiler would gather
+    // the additions), then copy_p(slot, c) is this wave's c-th copy.  The first
+    // of two halves ends in whole blocks too: P's codes behind it are zeros, and
+    // what Q's stage holds there are the second half's first rows (a half shorter
+    // than a stage: as many as it has, which drops no lane that the second needs).
+    __amdgpu_buffer_rsrc_t pr, qr, ur;
+    auto begin_p = [&](int st) {
+      const int left = st >= st1 ? 0 : a.halves == 2 ? BK : a.contract - st * BK;
 #pragma unroll
-      for (int c = 0; c < PI; ++c)
-        buffer_to_lds16(pr, dst + (wave * PI + c) * 1024, a.halves == 2 || pk[c] < left ? pv[c] : kNoLoad, 0);
-      const char* q = qbase + (Q_STR ? ((int64_t)half * a.contract + in * BK) * a.ldq : (int64_t)in * BK);
-      const __amdgpu_buffer_rsrc_t qr = buffer_at(q), ur = buffer_at(GATED ? q + (int64_t)F * a.ldq : q);
-#pragma unroll
-      for (int c = 0; c < QI; ++c)
-        buffer_to_lds16(GATED && (wave * QI + c) / 2 % 2 ? ur : qr, dst + kPBytes + (wave * QI + c) * 1024,
-                        qk[c] < left ? qv[c] : kNoLoad, 0);
+      for (int c = 0; c < PI; ++c) pv[c] = chunk_at(c) < left ? pv[c] : kNoLoad;
+      pr = buffer_at(pbase + (int64_t)st * BK);
     };
+    auto begin_q = [&](int st) {
+      const int half = st >= half_stages ? 1 : 0, in = st - half * half_stages;
+      const int left = st >= st1 ? 0 : a.contract * (a.halves - half) - in * BK;
+#pragma unroll
+      for (int c = 0; c < QI; ++c) qv[c] = (Q_STR ? q_at(c) : chunk_at(c)) < left ? qv[c] : kNoLoad;
+      const char* q = qbase + (Q_STR ? ((int64_t)half * a.contract + in * BK) * a.ldq : (int64_t)in * BK);
+      qr = buffer_at(q);
+      if (GATED) ur = buffer_at(q + (int64_t)F * a.ldq);
+    };
+    auto copy_p = [&](int slot, int c) { buffer_to_lds16(pr, smem + slot * kSlot + (wave * PI + c) * 1024, pv[c], 0); };
+    auto copy_q = [&](int slot, int c) {  // gated: the copy's 8 rows are gate or up
+      buffer_to_lds16(GATED && (wave * QI + c) / 2 % 2 ? ur : qr, smem + slot * kSlot + (wave * QI + c) * 1024, qv[c], 0);
+    };
+
     // ---- scales ----
     const float* psb = a.pscale + row0;
-    const float* qsb = a.qscale + (int64_t)t.group * a.qs_group +
-                       (int64_t)((n0 + (GATED ? 0 : wn * NJ * 16)) / kScaleBlock) * a.qs_cols;
-    // a block's last columns may lie past the matrix: their scale is not read
-    const bool cols_in = n0 + (GATED ? 0 : wn * NJ * 16) < ncols;
-    float ps[2][MI], qs[2][NS];
-    auto load_scales = [&](int b, int st) {
-      const __amdgpu_buffer_rsrc_t r = scales_at(psb + (int64_t)st * a.ldscale, live);
+    // (columns past the matrix take the first ones' scale: nothing of them is stored)
+    const int qcol = GATED || n0 + wn * NJ * 16 >= ncols ? n0 : n0 + wn * NJ * 16;
+    const float* qsb = a.qscale + (int64_t)t.group * a.qs_group + (int64_t)(qcol / kScaleBlock) * a.qs_cols;
+    const uint32_t prow = (wm * MI * 16 + l16) * 4;
+    __amdgpu_buffer_rsrc_t psr;
+    float ps[MI], qs[NS], qn[NS];  // of the rows to come (this stage's or the next), this stage's and the next one's columns
+    auto load_p = [&](int i) { ps[i] = load_scale(psr, prow + i * 64); };
+    auto load_q = [&](int st) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i) ps[b][i] = load_scale(r, ((wm * MI + i) * 16 + l16) * 4);
-#pragma unroll
-      for (int h = 0; h < NS; ++h) qs[b][h] = cols_in ? qsb[h * a.qs_half + st * a.qs_stage] : 0.0f;
+      for (int h = 0; h < NS; ++h)
+        qn[h] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+            buffer_at((const char*)(qsb + h * a.qs_half + (int64_t)min(st, st1 - 1) * a.qs_stage)), 0, 0, 0));
     };
+    auto begin_scales = [&](int st) { psr = scales_at(psb + (int64_t)min(st, st1 - 1) * a.ldscale, live); };
 
     // ---- fragments ----
+    typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+    // contiguous: lane l reads chunks l / 16 and 4 + l / 16 of row (row block) + l % 16
+    const int flo = l16 * BK + 16 * (quad ^ (l16 >> 1 & 7)), fhi = flo ^ 64;
+    // strided: lane l reads half of 16 columns of row 16 (l / 16) + l % 16 / 2 (+ 8, + 64, + 72)
+    int fat[NJ];
+    if constexpr (Q_STR) {
+      const int kr = quad * 16 + (l16 >> 1);
+      const int fold = BN == 256 ? (kr & 7) | (kr >> 1 & 8) : (kr >> 1 & 3) | (kr >> 2 & 4);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) fat[j] = kr * BN + 16 * ((wn * NJ + j) ^ fold) + 8 * (l16 & 1);
+    }
     auto pread = [&](int slot, int i) {
-      lds_char* at = smem + slot * kSlot + ((wm * MI + i) * 16 + l16) * BK;
-      const int sw = (l16 >> 1) & 7;
-      return join_halves(*(__attribute__((address_space(3))) u32x4*)(at + 16 * (quad ^ sw)),
-                         *(__attribute__((address_space(3))) u32x4*)(at + 16 * ((quad + 4) ^ sw)));
+      lds_char* at = smem + slot * kSlot + (wm * MI + i) * 16 * BK;
+      return join_halves(*(lds_u32x4*)(at + flo), *(lds_u32x4*)(at + fhi));
     };
     auto qread = [&](int slot, int j) {
-      lds_char* base = smem + slot * kSlot + kPBytes;
+      lds_char* at = smem + slot * kSlot;
       if constexpr (Q_STR) {
-        // lane l reads half of 16 columns of row 16 (l / 16) + l % 16 / 2 (+ 8, + 64)
-        u32x2 v[4];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int kr = (s / 2) * 64 + quad * 16 + (s % 2) * 8 + (l16 >> 1);
-          const int fold = BN == 256 ? (kr & 7) | (kr >> 1 & 8) : (kr >> 1 & 3) | (kr >> 2 & 4);
-          v[s] = read_transposed8(base + kr * BN + 16 * ((wn * NJ + j) ^ fold) + 8 * (l16 & 1));
-        }
-        return join_halves(u32x4{v[0].x, v[0].y, v[1].x, v[1].y}, u32x4{v[2].x, v[2].y, v[3].x, v[3].y});
+        at += fat[j];
+        const u32x2 v0 = read_transposed8(at), v1 = read_transposed8(at + 8 * BN);
+        const u32x2 v2 = read_transposed8(at + 64 * BN), v3 = read_transposed8(at + 72 * BN);
+        return join_halves(u32x4{v0.x, v0.y, v1.x, v1.y}, u32x4{v2.x, v2.y, v3.x, v3.y});
       } else {
-        lds_char* at = base + ((wn * NJ + j) * 16 + l16) * BK;
-        const int sw = (l16 >> 1) & 7;
-        return join_halves(*(__attribute__((address_space(3))) u32x4*)(at + 16 * (quad ^ sw)),
-                           *(__attribute__((address_space(3))) u32x4*)(at + 16 * ((quad + 4) ^ sw)));
+        at += (wn * NJ + j) * 16 * BK;
+        return join_halves(*(lds_u32x4*)(at + flo), *(lds_u32x4*)(at + fhi));
       }
     };
 
+    const int nst = st1 - st0;
     const bool busy = wm * MI * 16 < live;  // this wave has rows
-    copy_stage(0, st0);
-    load_scales(0, st0);
-    auto stage = [&](int b, int st) {
-      wait_copies<0>();
-      __syncthreads();  // stage st has landed, and the other slot is free
-      if (st + 1 < st1) {
-        copy_stage(b ^ 1, st + 1);
-        load_scales(b ^ 1, st + 1);
-      }
-      if (busy) {
-        i32x8 q[NJ];
+    begin_p(st0);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) q[j] = qread(b, j);
+    for (int c = 0; c < PI; ++c) copy_p(0, c);
+    begin_q(st0);
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          const i32x8 p = pread(b, i);
+    for (int c = 0; c < QI; ++c) copy_q(1, c);
+    begin_scales(st0);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) load_p(i);
+    load_q(st0);
+    begin_p(st0 + 1);
+#pragma unroll
+    for (int c = 0; c < PI; ++c) copy_p(2, c);
+    begin_q(st0 + 1);
+#pragma unroll
+    for (int c = 0; c < QI; ++c) copy_q(3, c);
+    __builtin_amdgcn_sched_barrier(0);
+    wait_copies<PI + QI>();
+    lds_only_barrier();
+    // Iteration i: slots pc and qc hold stage i, pn and qnx stage i + 1, `spare`
+    // is free and takes P's stage i + 2 during the first row blocks.  At the
+    // turn, before the last two row blocks (all of stage i's fragments are in
+    // registers by then), every wave has to be done with stage i and stage i + 1
+    // to have landed: pc takes Q's stage i + 2, and qc is the next spare one.
+    // A tile's products are added to the sums, scaled, while the next three
+    // tiles' are under way.
+    int pc = 0, qc = 1, pnx = 2, qnx = 3, spare = 4;
+    auto rotate = [&]() {
+      const int p = pc, q = qc;
+      pc = pnx;
+      qc = qnx;
+      pnx = spare;
+      qnx = p;
+      spare = q;
+    };
+    if (busy) {
+      i32x8 pf[R], qf[NJ];
+      f32x4 d[4] = {};
+      float sc[2][NS] = {};  // the scales of this row block and of the one before
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) qf[j] = qread(qc, j);
+#pragma unroll
+      for (int i = 0; i < R; ++i) pf[i] = pread(pc, i);
+      for (int i = 0; i < nst; ++i) {
+        begin_p(st0 + i + 2);
+        begin_scales(st0 + i + 1);
+#pragma unroll
+        for (int h = 0; h < NS; ++h) qs[h] = qn[h];
+        load_q(st0 + i + 1);
+#pragma unroll
+        for (int m = 0; m < MI; ++m) {
+          if (m == kTurn) {
+            wait_copies<PI + kTurn + NS>();
+            lds_only_barrier();
+            begin_q(st0 + i + 2);
+#pragma unroll
+            for (int r = 0; r < R - 2; ++r) pf[r] = pread(pnx, r);
+          }
+#pragma unroll
+          for (int h = 0; h < NS; ++h) sc[m & 1][h] = ps[m] * qs[h];
+          load_p(m);
+#pragma unroll
+          for (int c = kPCopies * m; c < kPCopies * (m + 1) && c < PI; ++c) copy_p(spare, c);
+          if (m >= kTurn) {
+            copy_q(pc, 2 * (m - kTurn));
+            copy_q(pc, 2 * (m - kTurn) + 1);
+          }
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
-            const f32x4 d = block_product(q[j], p);
-            const float s = ps[b][i] * qs[b][GATED ? j % 2 : 0];
+            __builtin_amdgcn_sched_barrier(0);
+            d[j] = block_product(qf[j], pf[m % R]);
+            // the tile three before: of this row block, or of the one before
+            const int b = (j + 1) % NJ, row = j == 3 ? m : (m + MI - 1) % MI;
+            const float s = sc[row & 1][GATED ? b % 2 : 0];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[e], s, acc[i][j][e]);
+            for (int e = 0; e < 4; ++e) acc[row][b][e] = fmaf(d[b][e], s, acc[row][b][e]);
+            if (m == MI - 1) qf[j] = qread(qnx, j);
           }
+          __builtin_amdgcn_sched_barrier(0);
+          if (m + R < MI) pf[m % R] = pread(pc, m + R);
+          if (m >= kTurn) pf[m % R] = pread(pnx, m % R);
         }
+        rotate();
       }
-    };
-    for (int st = st0; st < st1; st += 2) {
-      stage(0, st);
-      if (st + 1 < st1) stage(1, st + 1);
+#pragma unroll
+      for (int b = 1; b < NJ; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[MI - 1][b][e] = fmaf(d[b][e], sc[(MI - 1) & 1][GATED ? b % 2 : 0], acc[MI - 1][b][e]);
+    } else {
+      // a wave without rows only copies
+      for (int i = 0; i < nst; ++i) {
+        begin_p(st0 + i + 2);
+#pragma unroll
+        for (int c = 0; c < PI; ++c) copy_p(spare, c);
+        wait_copies<PI>();
+        lds_only_barrier();
+        begin_q(st0 + i + 2);
+#pragma unroll
+        for (int c = 0; c < QI; ++c) copy_q(pc, c);
+        rotate();
+      }
     }
+    wait_copies<0>();  // the zeros of stages past the end
     if (parts > 1) {
 #pragma unroll
       for (int i = 0; i < MI; ++i)
