@@ -108,18 +108,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
     // of two halves ends in whole blocks too: P's codes behind it are zeros, and
     // what Q's stage holds there are the second half's first rows (a half shorter
     // than a stage: as many as it has, which drops no lane that the second needs).
+    const int plen = a.halves == 2 ? stages * BK : a.contract;  // of P's rows
     __amdgpu_buffer_rsrc_t pr, qr, ur;
     auto begin_p = [&](int st) {
-      const int left = st >= st1 ? 0 : a.halves == 2 ? BK : a.contract - st * BK;
+      const int left = min(plen, st1 * BK) - st * BK;
 #pragma unroll
       for (int c = 0; c < PI; ++c) pv[c] = chunk_at(c) < left ? pv[c] : kNoLoad;
       pr = buffer_at(pbase + (int64_t)st * BK);
     };
     auto begin_q = [&](int st) {
       const int half = st >= half_stages ? 1 : 0, in = st - half * half_stages;
-      const int left = st >= st1 ? 0 : a.contract * (a.halves - half) - in * BK;
+      const int left = min(a.contract * (a.halves - half) - in * BK, (st1 - st) * BK);
 #pragma unroll
-      for (int c = 0; c < QI; ++c) qv[c] = (Q_STR ? q_at(c) : chunk_at(c)) < left ? qv[c] : kNoLoad;
+      for (int c = 0; c < QI; ++c)
+        qv[c] = (Q_STR ? q_at(0) : chunk_at(c)) < left - (Q_STR ? c * (64 / cpr) : 0) ? qv[c] : kNoLoad;
       const char* q = qbase + (Q_STR ? ((int64_t)half * a.contract + in * BK) * a.ldq : (int64_t)in * BK);
       qr = buffer_at(q);
       if (GATED) ur = buffer_at(q + (int64_t)F * a.ldq);
@@ -151,12 +153,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
     // contiguous: lane l reads chunks l / 16 and 4 + l / 16 of row (row block) + l % 16
     const int flo = l16 * BK + 16 * (quad ^ (l16 >> 1 & 7)), fhi = flo ^ 64;
     // strided: lane l reads half of 16 columns of row 16 (l / 16) + l % 16 / 2 (+ 8, + 64, + 72)
-    int fat[NJ];
+    int fat = 0;  // of column tile 0; another's differs in two bits of the chunk
     if constexpr (Q_STR) {
       const int kr = quad * 16 + (l16 >> 1);
       const int fold = BN == 256 ? (kr & 7) | (kr >> 1 & 8) : (kr >> 1 & 3) | (kr >> 2 & 4);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) fat[j] = kr * BN + 16 * ((wn * NJ + j) ^ fold) + 8 * (l16 & 1);
+      fat = kr * BN + 16 * ((wn * NJ) ^ fold) + 8 * (l16 & 1);
     }
     auto pread = [&](int slot, int i) {
       lds_char* at = smem + slot * kSlot + (wm * MI + i) * 16 * BK;
@@ -165,7 +166,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
     auto qread = [&](int slot, int j) {
       lds_char* at = smem + slot * kSlot;
       if constexpr (Q_STR) {
-        at += fat[j];
+        at = smem + ((slot * kSlot + fat) ^ (16 * j));
         const u32x2 v0 = read_transposed8(at), v1 = read_transposed8(at + 8 * BN);
         const u32x2 v2 = read_transposed8(at + 64 * BN), v3 = read_transposed8(at + 72 * BN);
         return join_halves(u32x4{v0.x, v0.y, v1.x, v1.y}, u32x4{v2.x, v2.y, v3.x, v3.y});
