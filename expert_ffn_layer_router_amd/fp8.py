@@ -62,13 +62,19 @@ def _weights(w, gated):
 
 def _operands(c, codes, scale, w, w_scale, rows, width):
     """(codes, their stride, scale, its stride, w, w_scale) as pointers."""
-    e4m3 = c.env.torch.float8_e4m3fn
+    env = c.env
+    e4m3 = env.e4m3
+    shape = w.shape
     pc, ldc = c.rows("codes", codes, rows, width, e4m3)
-    blocks = _blocks(width)
-    ps, lds = c.rows("scale", scale, blocks, rows, c.env.float32)
-    pw = c.plain("w", w, w.shape, e4m3)
-    pws = c.plain("w_scale", w_scale, (*w.shape[:-2], _blocks(w.shape[-2]), _blocks(w.shape[-1])), c.env.float32)
-    return pc, ldc, ps, max(lds, rows), pw, pws
+    ps, lds = c.rows("scale", scale, (width + 127) // BLOCK, rows, env.float32)
+    pw = c.plain("w", w, shape, e4m3)
+    pws = c.plain("w_scale", w_scale, _scale_shape(shape), env.float32)
+    return pc, ldc, ps, lds if lds > rows else rows, pw, pws
+
+
+@lru_cache(maxsize=1024)
+def _scale_shape(shape):
+    return (*shape[:-2], _blocks(shape[-2]), _blocks(shape[-1]))
 
 
 def quantize_blocks(x, tiles=False, codes=None, scale=None, stream=None):
@@ -77,11 +83,12 @@ def quantize_blocks(x, tiles=False, codes=None, scale=None, stream=None):
     (moe_quantize_blocks).  With `tiles`, weights x [..., n, k] have blocks of 128 x 128, scale
     [..., ceil(n / 128), ceil(k / 128)] (moe_quantize_tiles; x, codes and scale contiguous): the gated
     block's as [groups, 2, n, k]."""
-    e4m3 = _env().torch.float8_e4m3fn
+    e4m3 = _env().e4m3
     if not tiles:
         rows = _matrix_rows("x", x)
         k = x.shape[1]
-        _fits(rows=rows, k=k)
+        if rows | k > 0x7FFFFFFF:
+            _fits(rows=rows, k=k)
         with _Call(x, stream) as c:
             px, ldx = c.rows("x", x, rows, k, x.dtype)
             codes, pc, ldc = c.result("codes", codes, rows, k, e4m3)
@@ -94,7 +101,7 @@ def quantize_blocks(x, tiles=False, codes=None, scale=None, stream=None):
     n, k = x.shape[-2:]
     matrices = x[..., 0, 0].numel() if n and k else 0
     _fits(matrices=matrices, n=n, k=k)
-    shape = (*x.shape[:-2], _blocks(n), _blocks(k))
+    shape = _scale_shape(x.shape)
     with _Call(x, stream) as c:
         px = c.plain("x", x, x.shape, x.dtype)
         if codes is None:
@@ -178,8 +185,8 @@ def fp8_gated_backward(dh, gate_up, w, w_scale, offsets=None, activation="silu",
     with _Call(dh, stream) as c:
         pd, ldd = c.rows("dh", dh, rows, n, dtype)
         pg, ldg = c.rows("gate_up", gate_up, rows, 2 * n, dtype)
-        pw = c.plain("w", w, w.shape, c.env.torch.float8_e4m3fn)
-        pws = c.plain("w_scale", w_scale, (*w.shape[:-2], _blocks(n), _blocks(k)), c.env.float32)
+        pw = c.plain("w", w, w.shape, c.env.e4m3)
+        pws = c.plain("w_scale", w_scale, _scale_shape(w.shape), c.env.float32)
         po = c.offsets(offsets, groups)
         shape, need = _shape(_lib.MOE_FP8_OPS["fp8_gated_backward"], rows, n, k, groups, _type(dtype),
                              _act(activation))

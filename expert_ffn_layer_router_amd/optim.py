@@ -66,40 +66,47 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
     if not params:
         return
     codes = m_scale is not None
+    count = len(params)
     n = _lib.MoeAdamw(0.0, betas[0], betas[1], eps, weight_decay, 1.0, int(seed) & 0xFFFFFFFFFFFFFFFF, 0,
                       8 if codes else 32, None, None, None)
-    table = (_lib.MoeAdamwTensor * len(params))()
     with _Call(params[0], stream) as c:
-        torch = c.env.torch
-        float32 = c.env.float32
-        m_type, v_type = (torch.float8_e4m3fn, torch.float8_e5m2) if codes else (float32, float32)
+        env = c.env
+        float32, types, plain = env.float32, env.types, c.plain
+        m_type, v_type = (env.e4m3, env.e5m2) if codes else (float32, float32)
 
         def number(name, value, dtype):
             """A number, or the pointer of one on the device."""
-            if isinstance(value, torch.Tensor):
+            if isinstance(value, env.torch.Tensor):
                 if value.numel() != 1:
                     raise ValueError(f"{name} must be one value, not {list(value.shape)}")
-                return 0, c.plain(name, value, value.shape, dtype)
+                return 0, plain(name, value, value.shape, dtype)
             return value, None
 
         n.lr, n.device_lr = number("lr", lr, float32)
         n.grad_scale, n.device_grad_scale = number("grad_scale", grad_scale, float32)
-        step, n.device_step = number("step", step, c.env.int32)
+        step, n.device_step = number("step", step, env.int32)
         if not 0 <= int(step) < 1 << 31:
             raise ValueError(f"step={step} is out of range")
         n.step = int(step)
-        for i, p in enumerate(params):
-            shape, g, t = p.shape, grads[i], table[i]
-            t.param = c.plain("params", p, shape, p.dtype)
-            t.grad = c.plain("grads", g, shape, g.dtype)
-            if master is not None and master[i] is not None:
-                t.master = c.plain("master", master[i], shape, float32)
-            t.m = c.plain("m", m[i], shape, m_type)
-            t.v = c.plain("v", v[i], shape, v_type)
-            t.count = count = p.numel()
+        # the C structs (7 pointers, the count, two 32-bit types) as 64-bit words: setting their fields one by one
+        # would take longer than the checks
+        table = []
+        wide = ms = vs = 0
+        for i in range(count):
+            p, g = params[i], grads[i]
+            shape, dtype = p.shape, p.dtype
+            values = p.numel()
+            if master is not None:
+                wide = 0 if master[i] is None else plain("master", master[i], shape, float32)
             if codes:
-                blocks = ((count + BLOCK - 1) // BLOCK,)
-                t.m_scale = c.plain("m_scale", m_scale[i], blocks, float32)
-                t.v_scale = c.plain("v_scale", v_scale[i], blocks, float32)
-            t.param_type, t.grad_type = _type(p.dtype), _type(g.dtype)
-        _lib.check(c.lib.moe_adamw_step(ctypes.byref(n), len(params), table, c.stream))
+                blocks = ((values + 127) // BLOCK,)
+                ms = plain("m_scale", m_scale[i], blocks, float32)
+                vs = plain("v_scale", v_scale[i], blocks, float32)
+            table += (plain("params", p, shape, dtype), plain("grads", g, shape, g.dtype), wide,
+                      plain("m", m[i], shape, m_type), plain("v", v[i], shape, v_type), ms, vs, values,
+                      (types[dtype] if dtype in types else _type(dtype))
+                      | (types[g.dtype] if g.dtype in types else _type(g.dtype)) << 32)
+        words = (ctypes.c_int64 * len(table))(*table)
+        _lib.check(c.lib.moe_adamw_step(ctypes.byref(n), count,
+                                        ctypes.cast(words, ctypes.POINTER(_lib.MoeAdamwTensor)), c.stream))
+    env.torch.autograd.graph.increment_version(params)

@@ -35,6 +35,7 @@ class _Torch:
         import torch
         self.torch = torch
         self.int8, self.float32, self.int32, self.bfloat16 = torch.int8, torch.float32, torch.int32, torch.bfloat16
+        self.e4m3, self.e5m2 = torch.float8_e4m3fn, torch.float8_e5m2
         self.types = {torch.bfloat16: _lib.MOE_TYPE_BF16, torch.float16: _lib.MOE_TYPE_FP16,
                       torch.float32: _lib.MOE_TYPE_FP32}
         self.current_device = torch.cuda.current_device
