@@ -131,7 +131,7 @@ def load():
         "moe_fp8_gated": (c_int, [product, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, sz, vp]),
         "moe_fp8_product_backward": (c_int, [product, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, sz, vp]),
         "moe_fp8_gated_backward": (c_int, [product, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, sz, vp]),
-        "moe_adamw_step": (c_int, [ctypes.POINTER(MoeAdamw), i32, ctypes.POINTER(MoeAdamwTensor), vp]),
+        "moe_adamw_step": (c_int, [ctypes.POINTER(MoeAdamw), i32, vp, vp]),  # a table of MoeAdamwTensor
         "moe_status_string": (ctypes.c_char_p, [c_int]),
         "moe_last_error": (ctypes.c_char_p, []),
     }

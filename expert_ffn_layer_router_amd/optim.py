@@ -12,10 +12,15 @@ made under torch.no_grad(), as every update of a leaf in place."""
 from __future__ import annotations
 
 import ctypes
+import struct
+from functools import lru_cache
+from itertools import chain
+from operator import attrgetter
 
 from . import _lib
 from .products import _Call, _type
 
+_dtype_of, _shape_of, _tracked = attrgetter("dtype"), attrgetter("shape"), attrgetter("requires_grad")
 BLOCK = 128  # values of an 8-bit state that share a scale
 
 
@@ -51,6 +56,22 @@ def _lists(**lists):
             raise ValueError(f"{name} has {len(tensors)} tensors, params {length}")
 
 
+@lru_cache(maxsize=64)
+def _words(count):
+    return struct.Struct(f"{count}q")
+
+
+def _column(c, name, tensors, shapes, dtype):
+    """Pointers of a list of contiguous tensors (dtype None: of any).  A step of many small tensors is bound by the
+    host: what is right costs a few passes over the list, and only what is not is looked at tensor by tensor."""
+    tensor = c.env.torch.Tensor
+    if (set(map(tensor.get_device, tensors)) != {c.index} or not all(map(tensor.is_contiguous, tensors))
+            or (dtype is not None and set(map(_dtype_of, tensors)) != {dtype}) or list(map(_shape_of, tensors)) != shapes
+            or c.other is not None or (any(map(_tracked, tensors)) and c.env.grad_enabled())):
+        return [c.plain(name, t, shape, dtype or t.dtype) for t, shape in zip(tensors, shapes)]
+    return list(map(tensor.data_ptr, tensors))
+
+
 def adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, master=None,
                m_scale=None, v_scale=None, grad_scale=1.0, seed=0, stream=None):
     """One step of AdamW with decoupled weight decay on lists of contiguous tensors:
@@ -71,7 +92,7 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
                       8 if codes else 32, None, None, None)
     with _Call(params[0], stream) as c:
         env = c.env
-        float32, types, plain = env.float32, env.types, c.plain
+        float32, plain = env.float32, c.plain
         m_type, v_type = (env.e4m3, env.e5m2) if codes else (float32, float32)
 
         def number(name, value, dtype):
@@ -88,25 +109,27 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
         if not 0 <= int(step) < 1 << 31:
             raise ValueError(f"step={step} is out of range")
         n.step = int(step)
+        shapes = list(map(_shape_of, params))
+        pointers = [_column(c, "params", params, shapes, None), _column(c, "grads", grads, shapes, None)]
+        if master is None:
+            pointers.append([0] * count)
+        else:
+            given = [i for i in range(count) if master[i] is not None]
+            wide = _column(c, "master", [master[i] for i in given], [shapes[i] for i in given], float32)
+            pointers.append([0] * count)
+            for i, at in zip(given, wide):
+                pointers[2][i] = at
+        pointers += [_column(c, "m", m, shapes, m_type), _column(c, "v", v, shapes, v_type)]
+        values = list(map(env.torch.Tensor.numel, params))
+        if codes:
+            blocks = [((x + 127) // BLOCK,) for x in values]
+            pointers += [_column(c, "m_scale", m_scale, blocks, float32), _column(c, "v_scale", v_scale, blocks, float32)]
+        else:
+            pointers += [[0] * count] * 2
+        types = {t: _type(t) for t in set(map(_dtype_of, params)) | set(map(_dtype_of, grads))}
+        kinds = [types[p.dtype] | types[g.dtype] << 32 for p, g in zip(params, grads)]
         # the C structs (7 pointers, the count, two 32-bit types) as 64-bit words: setting their fields one by one
         # would take longer than the checks
-        table = []
-        wide = ms = vs = 0
-        for i in range(count):
-            p, g = params[i], grads[i]
-            shape, dtype = p.shape, p.dtype
-            values = p.numel()
-            if master is not None:
-                wide = 0 if master[i] is None else plain("master", master[i], shape, float32)
-            if codes:
-                blocks = ((values + 127) // BLOCK,)
-                ms = plain("m_scale", m_scale[i], blocks, float32)
-                vs = plain("v_scale", v_scale[i], blocks, float32)
-            table += (plain("params", p, shape, dtype), plain("grads", g, shape, g.dtype), wide,
-                      plain("m", m[i], shape, m_type), plain("v", v[i], shape, v_type), ms, vs, values,
-                      (types[dtype] if dtype in types else _type(dtype))
-                      | (types[g.dtype] if g.dtype in types else _type(g.dtype)) << 32)
-        words = (ctypes.c_int64 * len(table))(*table)
-        _lib.check(c.lib.moe_adamw_step(ctypes.byref(n), count,
-                                        ctypes.cast(words, ctypes.POINTER(_lib.MoeAdamwTensor)), c.stream))
+        table = _words(9 * count).pack(*chain.from_iterable(zip(*pointers, values, kinds)))
+        _lib.check(c.lib.moe_adamw_step(ctypes.byref(n), count, table, c.stream))
     env.torch.autograd.graph.increment_version(params)
