@@ -76,37 +76,38 @@ __device__ __forceinline__ float scale_of(uint32_t top) {
 }
 
 // ---- rows ---------------------------------------------------------------------
-// A block of threads takes 16 rows of 4 scale blocks: a wave reads 1 KB of a row
-// at a time, and the scales leave as runs of 16 rows.
-constexpr int kQRows = 16, kQBlocks = 4;
+// A block of threads takes 4 PER rows of 4 scale blocks: a wave reads 1 KB of a
+// row at a time, and the scales leave as runs of 4 PER rows.
+constexpr int kBlocks = 4;  // scale blocks of a row that a wave covers
+template <int PER>
 __global__ __launch_bounds__(256) void quantize_blocks_kernel(int rows, int k, bool fp16, const uint16_t* __restrict__ x,
                                                               int64_t ldx, uint8_t* __restrict__ codes, int64_t ldcodes,
                                                               float* __restrict__ scale, int64_t ldscale) {
-  __shared__ float scales[kQBlocks][kQRows];
+  constexpr int kRows = 4 * PER;
+  __shared__ float scales[kBlocks][kRows];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int across = (scale_blocks(k) + kQBlocks - 1) / kQBlocks;
-  const int row0 = blockIdx.x / across * kQRows, kb0 = blockIdx.x % across * kQBlocks;
+  const int across = (scale_blocks(k) + kBlocks - 1) / kBlocks;
+  const int row0 = blockIdx.x / across * kRows, kb0 = blockIdx.x % across * kBlocks;
   const int col = kb0 * kScaleBlock + lane * 8;
-  constexpr int kPer = kQRows / 4;
-  u32x4 v[kPer];
+  u32x4 v[PER];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int row = row0 + wave * kPer + i;
+  for (int i = 0; i < PER; ++i) {
+    const int row = row0 + wave * PER + i;
     v[i] = row < rows && col < k ? *reinterpret_cast<const u32x4*>(x + (int64_t)row * ldx + col) : u32x4{};
   }
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int row = row0 + wave * kPer + i;
+  for (int i = 0; i < PER; ++i) {
+    const int row = row0 + wave * PER + i;
     const uint32_t top = max16(top_of(fp16, v[i]));
     const Coder code(top);
     const u32x2 w = code.eight(fp16, v[i]);
     if (row < rows && col < k) *reinterpret_cast<u32x2*>(codes + (int64_t)row * ldcodes + col) = w;
-    if ((lane & 15) == 0) scales[lane >> 4][wave * kPer + i] = scale_of(top);
+    if ((lane & 15) == 0) scales[lane >> 4][wave * PER + i] = scale_of(top);
   }
   __syncthreads();
-  if (tid < kQRows * kQBlocks) {
-    const int b = kb0 + tid / kQRows, row = row0 + tid % kQRows;
-    if (b * kScaleBlock < k && row < rows) scale[(int64_t)b * ldscale + row] = scales[tid / kQRows][tid % kQRows];
+  if (tid < kRows * kBlocks) {
+    const int b = kb0 + tid / kRows, row = row0 + tid % kRows;
+    if (b * kScaleBlock < k && row < rows) scale[(int64_t)b * ldscale + row] = scales[tid / kRows][tid % kRows];
   }
 }
 
@@ -146,7 +147,7 @@ __global__ __launch_bounds__(256) void quantize_tiles_kernel(int n, int k, bool 
 // dg = dh u act'(g), du = dh act(g) in fp32, from there into codes and, where
 // they are asked for (the weights' gradient takes them), into 16 bits.  Rows
 // before the first group and behind the last are skipped.
-constexpr int kSRows = 16, kSBlocks = 4;
+template <int PER>
 __global__ __launch_bounds__(256) void fp8_slopes_kernel(int rows, int n, bool fp16, int act,
                                                          const uint16_t* __restrict__ dh, int64_t lddh,
                                                          const uint16_t* __restrict__ gu, int64_t ldgu,
@@ -154,28 +155,28 @@ __global__ __launch_bounds__(256) void fp8_slopes_kernel(int rows, int n, bool f
                                                          uint16_t* __restrict__ slopes, int64_t ldslopes,
                                                          uint8_t* __restrict__ codes, float* __restrict__ scale,
                                                          int64_t ldscale) {
-  __shared__ float scales[2][kSBlocks][kSRows];
+  constexpr int kRows = 4 * PER;
+  __shared__ float scales[2][kBlocks][kRows];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int first = offsets ? max(offsets[0], 0) : 0;
   const int last = offsets ? min(offsets[groups], rows) : rows;
-  const int nb = scale_blocks(n), across = (nb + kSBlocks - 1) / kSBlocks;
-  const int row0 = blockIdx.x / across * kSRows, kb0 = blockIdx.x % across * kSBlocks;
-  if (row0 >= last || row0 + kSRows <= first) return;
+  const int nb = scale_blocks(n), across = (nb + kBlocks - 1) / kBlocks;
+  const int row0 = blockIdx.x / across * kRows, kb0 = blockIdx.x % across * kBlocks;
+  if (row0 >= last || row0 + kRows <= first) return;
   const int col = kb0 * kScaleBlock + lane * 8;
   const int64_t half = (int64_t)nb * kScaleBlock, ldcodes = 2 * half;
-  constexpr int kPer = kSRows / 4;
-  u32x4 d[kPer], g[kPer], u[kPer];
+  u32x4 d[PER], g[PER], u[PER];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int row = row0 + wave * kPer + i;
+  for (int i = 0; i < PER; ++i) {
+    const int row = row0 + wave * PER + i;
     const bool in = row >= first && row < last && col < n;
     d[i] = in ? *reinterpret_cast<const u32x4*>(dh + (int64_t)row * lddh + col) : u32x4{};
     g[i] = in ? *reinterpret_cast<const u32x4*>(gu + (int64_t)row * ldgu + col) : u32x4{};
     u[i] = in ? *reinterpret_cast<const u32x4*>(gu + (int64_t)row * ldgu + n + col) : u32x4{};
   }
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int row = row0 + wave * kPer + i;
+  for (int i = 0; i < PER; ++i) {
+    const int row = row0 + wave * PER + i;
     const bool in = row >= first && row < last;
     float dg[8], du[8];
     uint32_t gtop = 0, utop = 0;
@@ -209,26 +210,36 @@ __global__ __launch_bounds__(256) void fp8_slopes_kernel(int rows, int n, bool f
       *reinterpret_cast<u32x2*>(to + half) = u32x2{cu.four(du[0], du[1], du[2], du[3]), cu.four(du[4], du[5], du[6], du[7])};
     }
     if ((lane & 15) == 0) {
-      scales[0][lane >> 4][wave * kPer + i] = scale_of(gtop);
-      scales[1][lane >> 4][wave * kPer + i] = scale_of(utop);
+      scales[0][lane >> 4][wave * PER + i] = scale_of(gtop);
+      scales[1][lane >> 4][wave * PER + i] = scale_of(utop);
     }
   }
   if (!codes) return;
   __syncthreads();
-  if (tid < 2 * kSRows * kSBlocks) {
-    const int h = tid / (kSRows * kSBlocks), in = tid % (kSRows * kSBlocks);
-    const int b = kb0 + in / kSRows, row = row0 + in % kSRows;
-    if (b < nb && row < rows) scale[(int64_t)(h * nb + b) * ldscale + row] = scales[h][in / kSRows][in % kSRows];
+  if (tid < 2 * kRows * kBlocks) {
+    const int h = tid / (kRows * kBlocks), in = tid % (kRows * kBlocks);
+    const int b = kb0 + in / kRows, row = row0 + in % kRows;
+    if (b < nb && row < rows) scale[(int64_t)(h * nb + b) * ldscale + row] = scales[h][in / kRows][in % kRows];
   }
 }
+
+// Whether blocks of 16 rows leave compute units without one.
+bool few_blocks(int rows, int across) { return (int64_t)across * ((rows + 15) / 16) < 512; }
 
 }  // namespace
 
 void launch_quantize_blocks(int rows, int k, int type, const uint16_t* x, int64_t ldx, uint8_t* codes, int64_t ldcodes,
                             float* scale, int64_t ldscale, hipStream_t s) {
-  const int across = (scale_blocks(k) + kQBlocks - 1) / kQBlocks;
-  quantize_blocks_kernel<<<across * ((rows + kQRows - 1) / kQRows), 256, 0, s>>>(
-      rows, k, type == MOE_TYPE_FP16, x, ldx, codes, ldcodes, scale, ldscale);
+  const int across = (scale_blocks(k) + kBlocks - 1) / kBlocks;
+  auto go = [&](auto per) {
+    constexpr int P = decltype(per)::value;
+    quantize_blocks_kernel<P><<<across * ((rows + 4 * P - 1) / (4 * P)), 256, 0, s>>>(
+        rows, k, type == MOE_TYPE_FP16, x, ldx, codes, ldcodes, scale, ldscale);
+  };
+  if (few_blocks(rows, across))
+    go(std::integral_constant<int, 1>{});
+  else
+    go(std::integral_constant<int, 4>{});
 }
 
 void launch_quantize_tiles(int matrices, int n, int k, int type, const uint16_t* x, uint8_t* codes, float* scale,
@@ -240,10 +251,17 @@ void launch_quantize_tiles(int matrices, int n, int k, int type, const uint16_t*
 void launch_fp8_slopes(int rows, int n, int type, int act, const uint16_t* dh, int64_t lddh, const uint16_t* gate_up,
                        int64_t ldgu, const int32_t* offsets, int groups, uint16_t* slopes, int64_t ldslopes,
                        uint8_t* codes, float* scale, int64_t ldscale, hipStream_t s) {
-  const int across = (scale_blocks(n) + kSBlocks - 1) / kSBlocks;
-  fp8_slopes_kernel<<<across * ((rows + kSRows - 1) / kSRows), 256, 0, s>>>(
-      rows, n, type == MOE_TYPE_FP16, act, dh, lddh, gate_up, ldgu, offsets, groups, slopes, ldslopes, codes, scale,
-      ldscale);
+  const int across = (scale_blocks(n) + kBlocks - 1) / kBlocks;
+  auto go = [&](auto per) {
+    constexpr int P = decltype(per)::value;
+    fp8_slopes_kernel<P><<<across * ((rows + 4 * P - 1) / (4 * P)), 256, 0, s>>>(
+        rows, n, type == MOE_TYPE_FP16, act, dh, lddh, gate_up, ldgu, offsets, groups, slopes, ldslopes, codes, scale,
+        ldscale);
+  };
+  if (few_blocks(rows, across))
+    go(std::integral_constant<int, 1>{});
+  else
+    go(std::integral_constant<int, 4>{});
 }
 
 }  // namespace moe
