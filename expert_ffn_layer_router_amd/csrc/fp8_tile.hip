@@ -12,7 +12,7 @@ __device__ __forceinline__ u32x2 read_transposed8(lds_char* __restrict p) {
   typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)p));
 }
-template <Pass PASS, Result RES, bool JOIN, int BM, int BN, int WM, int WN>
+template <Pass PASS, Result RES, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
   constexpr int NW = WM * WN, THREADS = 64 * NW;
   constexpr int MI = BM / 16 / WM, NJ = BN / 16 / WN;
@@ -46,7 +46,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
   const int half_stages = (a.contract + BK - 1) / BK;
   const int stages = a.halves * half_stages;
   RowTile t;
-  if (!find_row_tile<BM, BN, THREADS, JOIN>(a, tiles_n, stages, smem, t)) return;
+  if (!find_row_tile<BM, BN, THREADS, false>(a, tiles_n, stages, smem, t)) return;
   const int row0 = t.row0, live = min(BM, t.end - t.row0), n0 = t.tile_n * NO;
   const int parts = t.parts;
   if (a.groups > 1) __syncthreads();  // the lookup's LDS is free
@@ -60,13 +60,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{};
-  if constexpr (JOIN) {
-    for (int s = 0; s < parts; ++s)
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] += *raw(t.slot + s * t.slot_step, i, j);
-  } else {
+  {
     // ---- copies ----
     const char* pbase = a.p + (int64_t)row0 * a.ldp;
     const char* qbase = a.q + (int64_t)t.group * a.q_group + (Q_STR ? (int64_t)n0 : (int64_t)n0 * a.ldq);
@@ -345,6 +339,52 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
   }
 }
 
+// Adds the raw sums of a split tile's parts, in order, and writes the result:
+// block (b, i) has the i-th 16 rows of each wave of the b-th split tile, so that
+// all compute units take part (64 tiles of 256 x 256 in 4 parts: 20 us as one
+// block a tile).
+template <Result RES, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void fp8_join_kernel(Fp8Args a) {
+  constexpr int THREADS = 64 * WM * WN, MI = BM / 16 / WM, NJ = BN / 16 / WN;
+  constexpr bool GATED = RES == Result::kGated;
+  constexpr int NO = GATED ? BN / 2 : BN;
+  __shared__ char scratch[32];
+  const int F = a.cols / 2, ncols = GATED ? F : a.cols;
+  const int stages = a.halves * scale_blocks(a.contract);
+  RowTile t;
+  if (!find_row_tile<BM, BN, THREADS, true>(a, (ncols + NO - 1) / NO, stages, (lds_char*)scratch, t)) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = blockIdx.y;
+  const int row = t.row0 + (wave / WN * MI + i) * 16 + (lane & 15);
+  if (row >= t.end) return;
+  const f32x4* from = reinterpret_cast<const f32x4*>(a.partial) + ((int64_t)(wave * MI + i) * NJ) * 64 + lane;
+  f32x4 v[NJ] = {};
+  for (int s = 0; s < t.parts; ++s) {
+    const f32x4* p = from + (int64_t)(t.slot + s * t.slot_step) * (BM * BN / 4);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) v[j] += p[j * 64];
+  }
+  const bool fp16 = a.out_type == MOE_TYPE_FP16;
+  auto store = [&](uint16_t* p, f32x4 x) {
+    *reinterpret_cast<u32x2*>(p) = u32x2{pack_half(fp16, x[0], x[1]), pack_half(fp16, x[2], x[3])};
+  };
+  const int c0 = t.tile_n * NO + wave % WN * (NO / WN) + 4 * (lane >> 4);
+#pragma unroll
+  for (int j = 0; j < NJ; j += GATED ? 2 : 1) {
+    const int c = c0 + (GATED ? j / 2 : j) * 16;
+    if (c >= ncols) continue;
+    f32x4 x = v[j];
+    if constexpr (GATED) {
+      if (a.keep) {
+        store(a.keep + (int64_t)row * a.ldkeep + c, x);
+        store(a.keep + (int64_t)row * a.ldkeep + F + c, v[j + 1]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = activate(a.act, x[e]) * v[j + 1][e];
+    }
+    store((uint16_t*)a.out + (int64_t)row * a.ldout + c, x);
+  }
+}
+
 template <Pass PASS, Result RES, int BM, int BN, int WM, int WN>
 void launch_tile8(const Fp8Args& a, hipStream_t s) {
   const int no = RES == Result::kGated ? BN / 2 : BN;
@@ -352,8 +392,8 @@ void launch_tile8(const Fp8Args& a, hipStream_t s) {
   const int tiles = row_tile_bound(a.rows, a.groups, BM) * tiles_n;
   const int blocks = (tiles + 7) / 8 * 8 + (a.splits > 1 ? split_units(BM, tiles, a.splits) + 8 : 0);
   const int joins = std::min(tiles, (BM == 256 ? 256 : 512) / 2);  // a split tile has at least two parts
-  fp8_tile_kernel<PASS, RES, false, BM, BN, WM, WN><<<blocks, 64 * WM * WN, 0, s>>>(a);
-  if (a.splits > 1) fp8_tile_kernel<PASS, RES, true, BM, BN, WM, WN><<<joins, 64 * WM * WN, 0, s>>>(a);
+  fp8_tile_kernel<PASS, RES, BM, BN, WM, WN><<<blocks, 64 * WM * WN, 0, s>>>(a);
+  if (a.splits > 1) fp8_join_kernel<RES, BM, BN, WM, WN><<<dim3(joins, BM / 16 / WM), 64 * WM * WN, 0, s>>>(a);
 }
 
 template <Pass PASS, Result RES>
