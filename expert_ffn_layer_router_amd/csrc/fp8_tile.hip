@@ -292,7 +292,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
   {
     const bool fp16 = a.out_type == MOE_TYPE_FP16;
     uint16_t* outp = (uint16_t*)a.out;
-    __syncthreads();  // the stages' LDS is free
+    // barriers that leave the stores in flight: nothing waits for them but the
+    // kernel's end
+    lds_only_barrier();  // the stages' LDS is free
     // LDS rows of `width` values, 16-byte chunks swizzled by the row
     auto put = [&](int width, int row, int col, f32x4 v) {
       const u32x2 h = {pack_half(fp16, v[0], v[1]), pack_half(fp16, v[2], v[3])};
@@ -313,7 +315,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
         }
         put(NO, rowl(i), coll(j), v);
       }
-    __syncthreads();
+    lds_only_barrier();
     for (int x = tid; x < BM * (NO / 8); x += THREADS) {
       const int r = x / (NO / 8), c = x % (NO / 8);
       if (r < live && n0 + 8 * c < ncols)
@@ -321,18 +323,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
     }
     if constexpr (GATED) {
       if (a.keep) {
-        __syncthreads();
-        // gate columns in the left half of the LDS rows, up in the right
+        lds_only_barrier();
+        // gate columns in the left half of the LDS rows, up in the right; not to be
+        // read before the backward pass, so the caches need not keep them
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
           for (int j = 0; j < NJ; ++j) put(BN, rowl(i), coll(j) + (j % 2 ? NO : 0), acc[i][j]);
-        __syncthreads();
+        lds_only_barrier();
         for (int x = tid; x < BM * (BN / 8); x += THREADS) {
           const int r = x / (BN / 8), c = x % (BN / 8);
           const int up = c >= NO / 8, col = n0 + 8 * (c - up * (NO / 8));
           if (r < live && col < F)
-            *reinterpret_cast<u32x4*>(a.keep + ((int64_t)row0 + r) * a.ldkeep + up * F + col) = get(BN, r, c);
+            __builtin_nontemporal_store(get(BN, r, c), reinterpret_cast<u32x4*>(
+                                                           a.keep + ((int64_t)row0 + r) * a.ldkeep + up * F + col));
         }
       }
     }
