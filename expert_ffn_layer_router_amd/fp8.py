@@ -69,7 +69,7 @@ def _operands(c, codes, scale, w, w_scale, rows, width):
     ps, lds = c.rows("scale", scale, (width + 127) // BLOCK, rows, env.float32)
     pw = c.plain("w", w, shape, e4m3)
     pws = c.plain("w_scale", w_scale, _scale_shape(shape), env.float32)
-    return pc, ldc, ps, lds if lds > rows else rows, pw, pws
+    return pc, ldc, ps, lds, pw, pws
 
 
 @lru_cache(maxsize=1024)
@@ -93,7 +93,7 @@ def quantize_blocks(x, tiles=False, codes=None, scale=None, stream=None):
             px, ldx = c.rows("x", x, rows, k, x.dtype)
             codes, pc, ldc = c.result("codes", codes, rows, k, e4m3)
             scale, ps, lds = c.result("scale", scale, _blocks(k), rows, c.env.float32)
-            _lib.check(c.lib.moe_quantize_blocks(rows, k, _type(x.dtype), px, ldx, pc, ldc, ps, max(lds, rows),
+            _lib.check(c.lib.moe_quantize_blocks(rows, k, _type(x.dtype), px, ldx, pc, ldc, ps, lds,
                                                  c.stream))
         return codes, scale
     if x.dim() < 2:

@@ -132,4 +132,5 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
         # would take longer than the checks
         table = _words(9 * count).pack(*chain.from_iterable(zip(*pointers, values, kinds)))
         _lib.check(c.lib.moe_adamw_step(ctypes.byref(n), count, table, c.stream))
-    env.torch.autograd.graph.increment_version(params)
+    # autograd then refuses a backward pass through what the step has overwritten (inference tensors take part in none)
+    env.torch.autograd.graph.increment_version([p for p in params if not p.is_inference()])

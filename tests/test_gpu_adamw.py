@@ -345,3 +345,51 @@ def test_streams_and_refusals(torch, moe):
     torch.cuda.synchronize()
     assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(s.state(), before))
     moe.adamw_step([], [], [], [], 1)
+
+
+def test_versions_views_and_scalars(torch, moe):
+    """Autograd sees that a step overwrote its leaves; views need their alignment; a tensor may have no dimension."""
+    from expert_ffn_layer_router_amd import MoeError
+    p = torch.ones(4, device="cuda", requires_grad=True)
+    y = (p * p).sum()
+    states = moe.adamw_states([p])
+    with torch.no_grad():
+        moe.adamw_step([p], [torch.ones(4, device="cuda")], step=1, **states)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        q = torch.ones(4, device="cuda")
+        moe.adamw_step([q], [torch.ones(4, device="cuda")], step=1, **moe.adamw_states([q]))
+        assert torch.equal(q, p)
+    one = [torch.tensor(1.0, device="cuda")]
+    moe.adamw_step(one, [torch.tensor(1.0, device="cuda")], step=1, **moe.adamw_states(one))
+    assert one[0].item() == p[0].item()
+    buf = torch.ones(16, device="cuda")
+    view = [buf[1:9]]
+    with pytest.raises(MoeError, match="aligned"):
+        moe.adamw_step(view, [torch.ones(8, device="cuda")], step=1, **moe.adamw_states(view))
+    view = [buf[4:12]]
+    moe.adamw_step(view, [torch.ones(8, device="cuda")], step=1, **moe.adamw_states(view))
+    assert (buf[:4] == 1).all() and (buf[12:] == 1).all() and torch.equal(buf[4:8], p.detach())
+
+
+def test_past_32_bits(torch, moe):
+    """A tensor of more than 2^32 values: the last ones, and the first behind 2^32."""
+    n = (1 << 32) + 1000
+    tail = 5000
+    p = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    p[-tail:] = torch.randn(tail, device="cuda").to(torch.bfloat16)
+    g[-tail:] = torch.randn(tail, device="cuda").to(torch.bfloat16)
+    old = p[-tail:].clone()
+    states = moe.adamw_states([p], bits=8)
+    moe.adamw_step([p], [g], step=1, seed=1, **states, **HYPER)
+    # a first step: m = 0.1 g and v = 0.001 g^2 before their rounding, so each weight moves by lr against its gradient's sign
+    w = old.double() * (1 - HYPER["lr"] * HYPER["weight_decay"]) - HYPER["lr"] * torch.sign(g[-tail:].double())
+    assert ((p[-tail:].double() - w).abs() <= 2.0 ** -8 * w.abs() * 1.01 + 100 * E + 1e-3 * HYPER["lr"]).all()
+    assert not p[:-tail].any() and not states["m"][0].view(torch.uint8)[:-tail].any()
+    m = states["m"][0][-tail:].double() * states["m_scale"][0].repeat_interleave(128)[:n][-tail:].double()
+    # an 8-bit state is one of its two neighbouring codes: within 2^-3 of itself, or 2^-9 of its scale
+    top = states["m_scale"][0].repeat_interleave(128)[:n][-tail:].double()
+    want = 0.1 * g[-tail:].double()
+    assert ((m - want).abs() <= 2.0 ** -3 * want.abs() * 1.01 + 2.0 ** -9 * top * 1.01).all()
