@@ -205,8 +205,7 @@ MOE_EXPORT moe_status moe_quantize_blocks(int32_t rows, int32_t k, int32_t type,
 MOE_EXPORT moe_status moe_quantize_tiles(int32_t matrices, int32_t n, int32_t k, int32_t type, const uint16_t* x,
                                          uint8_t* codes, float* scale, moe_stream stream) {
   MOE_TRY(check_values(n, kMaxWidth, k, type));
-  if (n < 16 || n % 16)
-    return api_fail(MOE_ERR_UNSUPPORTED_SHAPE, "n=%d must be a multiple of 16 in [16, %d]", n, kMaxWidth);
+  if (n < 1) return api_fail(MOE_ERR_UNSUPPORTED_SHAPE, "n=%d outside [1, %d]", n, kMaxWidth);
   if (matrices < 0 || matrices > 2 * kMaxGroups)
     return api_fail(MOE_ERR_UNSUPPORTED_SHAPE, "matrices=%d outside [0, %d]", matrices, 2 * kMaxGroups);
   if (matrices == 0) return MOE_OK;

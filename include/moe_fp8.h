@@ -69,7 +69,7 @@ moe_status moe_quantize_blocks(int32_t rows, int32_t k, int32_t type, const uint
                                int64_t ldcodes, float *scale, int64_t ldscale, moe_stream stream);
 
 /* x, codes [matrices][n][k], scale [matrices][nb][kb], all contiguous;
- * matrices 0 .. 512, n a multiple of 16 in 16 .. 65536. */
+ * matrices 0 .. 512, n 1 .. 65536 (the products take multiples of 16). */
 moe_status moe_quantize_tiles(int32_t matrices, int32_t n, int32_t k, int32_t type, const uint16_t *x, uint8_t *codes,
                               float *scale, moe_stream stream);
 

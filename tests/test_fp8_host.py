@@ -147,7 +147,7 @@ def test_quantize_arguments_refused(lib):
         return lib.moe_quantize_tiles(matrices, n, k, type_, x, codes, scale, None)
 
     assert tiles(matrices=0, x=None, codes=None, scale=None) == 0
-    for kw in (dict(matrices=-1), dict(matrices=513), dict(n=0), dict(n=24), dict(n=65552), dict(k=0), dict(k=24),
+    for kw in (dict(matrices=-1), dict(matrices=513), dict(n=0), dict(n=-16), dict(n=65537), dict(k=0), dict(k=24),
                dict(type_=FP32)):
         assert tiles(**kw) == SHAPE, kw
     for kw in (dict(x=None), dict(x=FAKE + 8), dict(codes=None), dict(codes=FAKE + 8), dict(scale=None),

@@ -320,7 +320,8 @@ def test_quantize_blocks_every_value(torch, moe, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("shape", [(16, 16), (128, 128), (144, 400), (3, 272, 144), (2, 2, 400, 1040), (1, 1008, 4112)])
+@pytest.mark.parametrize("shape", [(16, 16), (128, 128), (144, 400), (3, 272, 144), (2, 2, 400, 1040), (1, 1008, 4112), (1, 48), (84, 144),
+                                   (3, 131, 272)])
 def test_quantize_tiles(torch, moe, shape, dtype):
     gen = torch.Generator(device="cuda").manual_seed(sum(shape))
     t = getattr(torch, dtype)
