@@ -130,17 +130,40 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
     // (columns past the matrix take the first ones' scale: nothing of them is stored)
     const int qcol = GATED || n0 + wn * NJ * 16 >= ncols ? n0 : n0 + wn * NJ * 16;
     const float* qsb = a.qscale + (int64_t)t.group * a.qs_group + (int64_t)(qcol / kScaleBlock) * a.qs_cols;
-    const uint32_t prow = (wm * MI * 16 + l16) * 4;
-    __amdgpu_buffer_rsrc_t psr;
-    float ps[MI], qs[NS], qn[NS];  // of the rows to come (this stage's or the next), this stage's and the next one's columns
-    auto load_p = [&](int i) { ps[i] = load_scale(psr, prow + i * 64); };
+    // a lane loads the scales of one row in 64, which go to the lanes that need
+    // them afterwards: the unit that returns data to the registers is as busy as
+    // the matrix cores, and every load costs it
+    constexpr int kLoads = MI / 4;
+    const uint32_t prow = (wm * MI * 16 + lane) * 4;
+    float pn[kLoads], qn[NS];  // the next stage's
+    float ps[MI], qs[NS];      // this one's
+    auto load_p = [&](int st) {
+      const __amdgpu_buffer_rsrc_t r = scales_at(psb + (int64_t)min(st, st1 - 1) * a.ldscale, live);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) pn[i] = load_scale(r, prow + i * 256);
+    };
+    auto take_scales = [&]() {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        // lanes 16 r .. of pn[i] hold row block 4 i + r: (r0 r0 r2 r2), (r1 r1 r3 r3), then each of them everywhere
+        const uint32_t v = __float_as_uint(pn[i]);
+        const auto even = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        const auto lo = __builtin_amdgcn_permlane32_swap(even[0], even[0], false, false);
+        const auto hi = __builtin_amdgcn_permlane32_swap(even[1], even[1], false, false);
+        ps[4 * i] = __uint_as_float(lo[0]);
+        ps[4 * i + 1] = __uint_as_float(hi[0]);
+        ps[4 * i + 2] = __uint_as_float(lo[1]);
+        ps[4 * i + 3] = __uint_as_float(hi[1]);
+      }
+#pragma unroll
+      for (int h = 0; h < NS; ++h) qs[h] = qn[h];
+    };
     auto load_q = [&](int st) {
 #pragma unroll
       for (int h = 0; h < NS; ++h)
         qn[h] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
             buffer_at((const char*)(qsb + h * a.qs_half + (int64_t)min(st, st1 - 1) * a.qs_stage)), 0, 0, 0));
     };
-    auto begin_scales = [&](int st) { psr = scales_at(psb + (int64_t)min(st, st1 - 1) * a.ldscale, live); };
 
     // ---- fragments ----
     typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
@@ -178,9 +201,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
     begin_q(st0);
 #pragma unroll
     for (int c = 0; c < QI; ++c) copy_q(1, c);
-    begin_scales(st0);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) load_p(i);
+    load_p(st0);
     load_q(st0);
     begin_p(st0 + 1);
 #pragma unroll
@@ -217,14 +238,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
       for (int i = 0; i < R; ++i) pf[i] = pread(pc, i);
       for (int i = 0; i < nst; ++i) {
         begin_p(st0 + i + 2);
-        begin_scales(st0 + i + 1);
-#pragma unroll
-        for (int h = 0; h < NS; ++h) qs[h] = qn[h];
+        take_scales();
+        load_p(st0 + i + 1);
         load_q(st0 + i + 1);
 #pragma unroll
         for (int m = 0; m < MI; ++m) {
           if (m == kTurn) {
-            wait_copies<PI + kTurn + NS>();
+            wait_copies<PI + kLoads + NS>();
             lds_only_barrier();
             begin_q(st0 + i + 2);
 #pragma unroll
@@ -232,7 +252,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
           }
 #pragma unroll
           for (int h = 0; h < NS; ++h) sc[m & 1][h] = ps[m] * qs[h];
-          load_p(m);
 #pragma unroll
           for (int c = kPCopies * m; c < kPCopies * (m + 1) && c < PI; ++c) copy_p(spare, c);
           if (m >= kTurn) {
