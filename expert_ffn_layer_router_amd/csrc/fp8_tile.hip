@@ -29,9 +29,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
   static_assert(NO % (16 * NJ / NS) == 0 && kScaleBlock % (16 * NJ / NS) == 0 && (!GATED || kScaleBlock % NO == 0),
                 "a wave's columns share a scale");
   static_assert(PI == QI && BM * BN * 2 <= kRing * kSlot, "equal slots; the 16-bit result fits the ring");
-  constexpr int R = 4;         // P fragments in registers
-  constexpr int kTurn = MI - 2;  // row blocks before the turn
-  constexpr int kPCopies = (PI + kTurn - 1) / kTurn;  // P copies of a row block before it
+  constexpr int R = MI == 8 ? 5 : 4;      // P fragments in registers
+  constexpr int kTurn = MI == 8 ? 4 : 1;  // row blocks before the turn
+  constexpr int kPCopies = (PI + kTurn - 1) / kTurn;                // P copies of a row block before it
+  constexpr int kQCopies = (QI + MI - kTurn - 1) / (MI - kTurn);    // Q copies of one after it
+  static_assert(kTurn >= MI - R && kTurn >= 1, "at the turn all of the stage's fragments are read");
   static_assert(MI >= R && NJ == 4 && PI == 4, "the rows' schedule");
   __shared__ __attribute__((aligned(1024))) char smem_raw[kRing * kSlot];
   lds_char* smem = (lds_char*)smem_raw;
@@ -248,15 +250,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
             lds_only_barrier();
             begin_q(st0 + i + 2);
 #pragma unroll
-            for (int r = 0; r < R - 2; ++r) pf[r] = pread(pnx, r);
+            for (int r = 0; r < R; ++r) {
+              bool used = false;  // by a row block to come
+              for (int to = kTurn; to < MI; ++to) used = used || to % R == r;
+              if (!used) pf[r] = pread(pnx, r);
+            }
           }
 #pragma unroll
           for (int h = 0; h < NS; ++h) sc[m & 1][h] = ps[m] * qs[h];
 #pragma unroll
           for (int c = kPCopies * m; c < kPCopies * (m + 1) && c < PI; ++c) copy_p(spare, c);
           if (m >= kTurn) {
-            copy_q(pc, 2 * (m - kTurn));
-            copy_q(pc, 2 * (m - kTurn) + 1);
+#pragma unroll
+            for (int c = kQCopies * (m - kTurn); c < kQCopies * (m - kTurn + 1) && c < QI; ++c) copy_q(pc, c);
           }
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
