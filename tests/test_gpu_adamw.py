@@ -200,6 +200,27 @@ def test_many_tensors(torch, moe, bits):
     compare(torch, s, expected)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-8, 1.0, 1e4])
+def test_any_eps(torch, moe, eps, bits):
+    """Gradients of 2^-62 to 2^4, whose v is subnormal below 2^-58: it is off by 2^-150 more, half of that through the
+    root."""
+    say(f"adamw eps {eps} {bits}")
+    s = Step(torch, [(1000,), (131,)], torch.float32, torch.float32, bits, False, moments=False)
+    gen = torch.Generator().manual_seed(3)
+    for g in s.grads:
+        g.copy_(torch.sign(torch.randn(g.shape, generator=gen)) * 2 ** (torch.rand(g.shape, generator=gen) * 66 - 62))
+    hyper = dict(HYPER, eps=eps)
+    expected = []
+    for g, (new, off, *rest) in zip(s.grads, s.expected(1, **hyper)):
+        g64 = g.double().cpu().numpy()
+        per = hyper["lr"] / (np.abs(g64) + eps) * np.abs(g64)
+        expected.append((new, off + per * 2.0 ** -151 / (1e-3 * g64 ** 2), *rest))
+    assert min(g.abs().min().item() for g in s.grads) < 2.0 ** -60
+    moe.adamw_step(step=1, **s.kwargs(), **hyper)
+    compare(torch, s, expected)
+
+
 def test_first_step_from_zero_states(torch, moe):
     for bits in (8, 32):
         s = Step(torch, [(300,), (2, 64)], torch.bfloat16, torch.float32, bits, True, moments=False)
