@@ -13,6 +13,11 @@
 //
 // Sixteen lanes hold a block, 8 values each, so its largest magnitude takes four
 // steps within a row of lanes.
+//
+// All three kernels are bound by memory: rows 8192 x 14336 take 66 to 80 us (4.5
+// to 5.4 TB/s, by how much of them the last-level cache still holds), 16 matrices
+// of 14336 x 4096 528 us (5.3 TB/s; a copy 4.9), the slopes of 4096 x 14336 with
+// their 16-bit copy 110 us (6.4 TB/s).
 #include <type_traits>
 
 #include "fp8_device.h"
@@ -77,8 +82,19 @@ __device__ __forceinline__ float scale_of(uint32_t top) {
 
 // ---- rows ---------------------------------------------------------------------
 // A block of threads takes 4 PER rows of 4 scale blocks: a wave reads 1 KB of a
-// row at a time, and the scales leave as runs of 4 PER rows.
+// row at a time, and the scales leave as runs of 4 PER rows.  One row a wave and
+// more blocks where there are few, two otherwise (us in a captured graph, 1 / 2 /
+// 4 rows): 16 x 4096 2.0 / 2.4 / 3.1, 512 x 4096 3.0 / 3.1 / 3.4, 1024 x 4096 4.2 /
+// 4.1 / 4.4, 16384 x 4096 35.2 / 32.5 / 35.5, 8192 x 14336 71.5 / 65.1 / 65.5.
 constexpr int kBlocks = 4;  // scale blocks of a row that a wave covers
+// The blocks of threads go across the columns first; a grid has fewer than 2^32
+// threads in x, which the largest matrices pass, so row blocks go on in y.
+constexpr int kRowBlocks = 1 << 16;
+__device__ __forceinline__ int row_block(int across) { return blockIdx.y * kRowBlocks + blockIdx.x / across; }
+dim3 row_grid(int rows, int per_block, int across) {
+  const int blocks = (rows + per_block - 1) / per_block;
+  return dim3(across * (blocks < kRowBlocks ? blocks : kRowBlocks), (blocks + kRowBlocks - 1) / kRowBlocks);
+}
 template <int PER>
 __global__ __launch_bounds__(256) void quantize_blocks_kernel(int rows, int k, bool fp16, const uint16_t* __restrict__ x,
                                                               int64_t ldx, uint8_t* __restrict__ codes, int64_t ldcodes,
@@ -87,7 +103,7 @@ __global__ __launch_bounds__(256) void quantize_blocks_kernel(int rows, int k, b
   __shared__ float scales[kBlocks][kRows];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int across = (scale_blocks(k) + kBlocks - 1) / kBlocks;
-  const int row0 = blockIdx.x / across * kRows, kb0 = blockIdx.x % across * kBlocks;
+  const int row0 = row_block(across) * kRows, kb0 = blockIdx.x % across * kBlocks;
   const int col = kb0 * kScaleBlock + lane * 8;
   u32x4 v[PER];
 #pragma unroll
@@ -146,8 +162,9 @@ __global__ __launch_bounds__(256) void quantize_tiles_kernel(int n, int k, bool 
 // ---- slopes of the gated block ------------------------------------------------
 // dg = dh u act'(g), du = dh act(g) in fp32, from there into codes and, where
 // they are asked for (the weights' gradient takes them), into 16 bits.  Rows
-// before the first group and behind the last are skipped.
-template <int PER>
+// before the first group and behind the last are skipped.  A wave takes one row's
+// 4 scale blocks: with two and four rows 4096 x 14336 took 3 and 9 us more, 24576 x
+// 2048 3 and 13, 300 x 1008 1.2 and 4.2 (three loads a row hold enough registers).
 __global__ __launch_bounds__(256) void fp8_slopes_kernel(int rows, int n, bool fp16, int act,
                                                          const uint16_t* __restrict__ dh, int64_t lddh,
                                                          const uint16_t* __restrict__ gu, int64_t ldgu,
@@ -155,66 +172,56 @@ __global__ __launch_bounds__(256) void fp8_slopes_kernel(int rows, int n, bool f
                                                          uint16_t* __restrict__ slopes, int64_t ldslopes,
                                                          uint8_t* __restrict__ codes, float* __restrict__ scale,
                                                          int64_t ldscale) {
-  constexpr int kRows = 4 * PER;
+  constexpr int kRows = 4;
   __shared__ float scales[2][kBlocks][kRows];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int first = offsets ? max(offsets[0], 0) : 0;
   const int last = offsets ? min(offsets[groups], rows) : rows;
   const int nb = scale_blocks(n), across = (nb + kBlocks - 1) / kBlocks;
-  const int row0 = blockIdx.x / across * kRows, kb0 = blockIdx.x % across * kBlocks;
+  const int row0 = row_block(across) * kRows, kb0 = blockIdx.x % across * kBlocks;
   if (row0 >= last || row0 + kRows <= first) return;
   const int col = kb0 * kScaleBlock + lane * 8;
   const int64_t half = (int64_t)nb * kScaleBlock, ldcodes = 2 * half;
-  u32x4 d[PER], g[PER], u[PER];
+  const int row = row0 + wave;
+  const bool in = row >= first && row < last, inside = in && col < n;
+  const u32x4 d = inside ? *reinterpret_cast<const u32x4*>(dh + (int64_t)row * lddh + col) : u32x4{};
+  const u32x4 g = inside ? *reinterpret_cast<const u32x4*>(gu + (int64_t)row * ldgu + col) : u32x4{};
+  const u32x4 u = inside ? *reinterpret_cast<const u32x4*>(gu + (int64_t)row * ldgu + n + col) : u32x4{};
+  float dg[8], du[8];
+  uint32_t gtop = 0, utop = 0;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int row = row0 + wave * PER + i;
-    const bool in = row >= first && row < last && col < n;
-    d[i] = in ? *reinterpret_cast<const u32x4*>(dh + (int64_t)row * lddh + col) : u32x4{};
-    g[i] = in ? *reinterpret_cast<const u32x4*>(gu + (int64_t)row * ldgu + col) : u32x4{};
-    u[i] = in ? *reinterpret_cast<const u32x4*>(gu + (int64_t)row * ldgu + n + col) : u32x4{};
+  for (int e = 0; e < 8; ++e) {
+    auto at = [&](u32x4 v) { return half_to_f32(fp16, (uint16_t)(v[e / 2] >> (16 * (e & 1)))); };
+    float value, slope;
+    activate_slope(act, at(g), value, slope);
+    dg[e] = at(d) * at(u) * slope;
+    du[e] = at(d) * value;
+    gtop = max(gtop, __float_as_uint(dg[e]) & 0x7FFFFFFFu);
+    utop = max(utop, __float_as_uint(du[e]) & 0x7FFFFFFFu);
   }
+  if (slopes && inside) {
+    u32x4 og, ou;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int row = row0 + wave * PER + i;
-    const bool in = row >= first && row < last;
-    float dg[8], du[8];
-    uint32_t gtop = 0, utop = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      auto at = [&](u32x4 v) { return half_to_f32(fp16, (uint16_t)(v[e / 2] >> (16 * (e & 1)))); };
-      float value, slope;
-      activate_slope(act, at(g[i]), value, slope);
-      dg[e] = at(d[i]) * at(u[i]) * slope;
-      du[e] = at(d[i]) * value;
-      gtop = max(gtop, __float_as_uint(dg[e]) & 0x7FFFFFFFu);
-      utop = max(utop, __float_as_uint(du[e]) & 0x7FFFFFFFu);
+    for (int e = 0; e < 4; ++e) {
+      og[e] = pack_half(fp16, dg[2 * e], dg[2 * e + 1]);
+      ou[e] = pack_half(fp16, du[2 * e], du[2 * e + 1]);
     }
-    if (slopes && in && col < n) {
-      u32x4 og, ou;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        og[e] = pack_half(fp16, dg[2 * e], dg[2 * e + 1]);
-        ou[e] = pack_half(fp16, du[2 * e], du[2 * e + 1]);
-      }
-      *reinterpret_cast<u32x4*>(slopes + (int64_t)row * ldslopes + col) = og;
-      *reinterpret_cast<u32x4*>(slopes + (int64_t)row * ldslopes + n + col) = ou;
-    }
-    if (!codes) continue;
-    gtop = max16(gtop);
-    utop = max16(utop);
-    const Coder cg(gtop), cu(utop);
-    if (in && col < half) {  // zeros behind the columns, up to whole blocks
-      uint8_t* to = codes + (int64_t)row * ldcodes + col;
-      *reinterpret_cast<u32x2*>(to) = u32x2{cg.four(dg[0], dg[1], dg[2], dg[3]), cg.four(dg[4], dg[5], dg[6], dg[7])};
-      *reinterpret_cast<u32x2*>(to + half) = u32x2{cu.four(du[0], du[1], du[2], du[3]), cu.four(du[4], du[5], du[6], du[7])};
-    }
-    if ((lane & 15) == 0) {
-      scales[0][lane >> 4][wave * PER + i] = scale_of(gtop);
-      scales[1][lane >> 4][wave * PER + i] = scale_of(utop);
-    }
+    *reinterpret_cast<u32x4*>(slopes + (int64_t)row * ldslopes + col) = og;
+    *reinterpret_cast<u32x4*>(slopes + (int64_t)row * ldslopes + n + col) = ou;
   }
   if (!codes) return;
+  gtop = max16(gtop);
+  utop = max16(utop);
+  const Coder cg(gtop), cu(utop);
+  if (in && col < half) {  // zeros behind the columns, up to whole blocks
+    uint8_t* to = codes + (int64_t)row * ldcodes + col;
+    *reinterpret_cast<u32x2*>(to) = u32x2{cg.four(dg[0], dg[1], dg[2], dg[3]), cg.four(dg[4], dg[5], dg[6], dg[7])};
+    *reinterpret_cast<u32x2*>(to + half) = u32x2{cu.four(du[0], du[1], du[2], du[3]), cu.four(du[4], du[5], du[6], du[7])};
+  }
+  if ((lane & 15) == 0) {
+    scales[0][lane >> 4][wave] = scale_of(gtop);
+    scales[1][lane >> 4][wave] = scale_of(utop);
+  }
   __syncthreads();
   if (tid < 2 * kRows * kBlocks) {
     const int h = tid / (kRows * kBlocks), in = tid % (kRows * kBlocks);
@@ -223,9 +230,6 @@ __global__ __launch_bounds__(256) void fp8_slopes_kernel(int rows, int n, bool f
   }
 }
 
-// Whether blocks of 16 rows leave compute units without one.
-bool few_blocks(int rows, int across) { return (int64_t)across * ((rows + 15) / 16) < 512; }
-
 }  // namespace
 
 void launch_quantize_blocks(int rows, int k, int type, const uint16_t* x, int64_t ldx, uint8_t* codes, int64_t ldcodes,
@@ -233,13 +237,13 @@ void launch_quantize_blocks(int rows, int k, int type, const uint16_t* x, int64_
   const int across = (scale_blocks(k) + kBlocks - 1) / kBlocks;
   auto go = [&](auto per) {
     constexpr int P = decltype(per)::value;
-    quantize_blocks_kernel<P><<<across * ((rows + 4 * P - 1) / (4 * P)), 256, 0, s>>>(
+    quantize_blocks_kernel<P><<<row_grid(rows, 4 * P, across), 256, 0, s>>>(
         rows, k, type == MOE_TYPE_FP16, x, ldx, codes, ldcodes, scale, ldscale);
   };
-  if (few_blocks(rows, across))
+  if ((int64_t)across * ((rows + 7) / 8) < 1024)
     go(std::integral_constant<int, 1>{});
   else
-    go(std::integral_constant<int, 4>{});
+    go(std::integral_constant<int, 2>{});
 }
 
 void launch_quantize_tiles(int matrices, int n, int k, int type, const uint16_t* x, uint8_t* codes, float* scale,
@@ -252,16 +256,8 @@ void launch_fp8_slopes(int rows, int n, int type, int act, const uint16_t* dh, i
                        int64_t ldgu, const int32_t* offsets, int groups, uint16_t* slopes, int64_t ldslopes,
                        uint8_t* codes, float* scale, int64_t ldscale, hipStream_t s) {
   const int across = (scale_blocks(n) + kBlocks - 1) / kBlocks;
-  auto go = [&](auto per) {
-    constexpr int P = decltype(per)::value;
-    fp8_slopes_kernel<P><<<across * ((rows + 4 * P - 1) / (4 * P)), 256, 0, s>>>(
-        rows, n, type == MOE_TYPE_FP16, act, dh, lddh, gate_up, ldgu, offsets, groups, slopes, ldslopes, codes, scale,
-        ldscale);
-  };
-  if (few_blocks(rows, across))
-    go(std::integral_constant<int, 1>{});
-  else
-    go(std::integral_constant<int, 4>{});
+  fp8_slopes_kernel<<<row_grid(rows, 4, across), 256, 0, s>>>(rows, n, type == MOE_TYPE_FP16, act, dh, lddh, gate_up, ldgu,
+                                                             offsets, groups, slopes, ldslopes, codes, scale, ldscale);
 }
 
 }  // namespace moe

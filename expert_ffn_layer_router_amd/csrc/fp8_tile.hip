@@ -33,7 +33,7 @@ __device__ __forceinline__ u32x2 read_transposed8(lds_char* __restrict p) {
 // random codes 432 us, 2545 TFLOP/s forward, 2510 input gradient and gated (a
 // large library product of plain 8-bit floats, without scales: 2630; integer
 // codes by this library, 2840); with all codes zero, where nothing switches and
-// the clock stays up, 321 us: the matrix cores are busy 68% of the cycles.
+// the clock stays up, 321 us: the matrix cores are busy 66% of the cycles.
 // Registers alone, the products reach 4350 TFLOP/s and with the FMAs 3650; the
 // FMAs cost 13% in the whole kernel too, the copies 25%, LDS reads 2%.  Each
 // step, timed at that size:

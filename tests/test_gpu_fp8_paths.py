@@ -429,6 +429,29 @@ def test_past_32_bits(torch, moe):
 
 # ---- gradients against differences --------------------------------------------------------
 
+def test_rows_past_a_grid(torch, moe):
+    """More rows than one dimension of the grid takes: 2^19 of quantize_blocks, 2^18 of the slopes.  Rows do not
+    depend on each other, so parts of them give the same bits."""
+    say("700001 rows")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(700001, 528, generator=gen, device="cuda").bfloat16()
+    codes, scale = moe.quantize_blocks(x)
+    for at in range(0, x.shape[0], 200000):
+        part, ps = moe.quantize_blocks(x[at:at + 200000])
+        assert torch.equal(bits(part), bits(codes[at:at + 200000]))
+        assert torch.equal(ps, scale[:, at:at + 200000])
+    del x, codes, scale
+    rows, n, k = 600001, 144, 16
+    dh = torch.randn(rows, n, generator=gen, device="cuda").bfloat16()
+    gate_up = torch.randn(rows, 2 * n, generator=gen, device="cuda").bfloat16()
+    w, ws = moe.quantize_blocks(torch.randn(1, 2, n, k, generator=gen, device="cuda").bfloat16(), tiles=True)
+    dx, slopes = moe.fp8_gated_backward(dh, gate_up, w, ws)
+    for at in range(0, rows, 200000):
+        pdx, ps = moe.fp8_gated_backward(dh[at:at + 200000], gate_up[at:at + 200000], w, ws)
+        assert torch.equal(pdx, dx[at:at + 200000])
+        assert torch.equal(ps, slopes[at:at + 200000])
+
+
 def test_product_gradient_against_differences(torch, moe):
     """Small whole codes and scales that are powers of two: every sum is exact in fp16, so that dx equals the
     differences of <dy, y> along each value of x, bit for bit."""
