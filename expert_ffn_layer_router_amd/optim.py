@@ -15,7 +15,7 @@ import ctypes
 import struct
 from functools import lru_cache
 from itertools import chain
-from operator import attrgetter
+from operator import attrgetter, index
 
 from . import _lib
 from .products import _Call, _type
@@ -106,9 +106,10 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
         n.lr, n.device_lr = number("lr", lr, float32)
         n.grad_scale, n.device_grad_scale = number("grad_scale", grad_scale, float32)
         step, n.device_step = number("step", step, env.int32)
-        if not 0 <= int(step) < 1 << 31:
+        step = index(step)
+        if not 0 <= step < 1 << 31:
             raise ValueError(f"step={step} is out of range")
-        n.step = int(step)
+        n.step = step
         shapes = list(map(_shape_of, params))
         pointers = [_column(c, "params", params, shapes, None), _column(c, "grads", grads, shapes, None)]
         if master is None:

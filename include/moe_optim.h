@@ -10,12 +10,13 @@
  *
  * in fp32.  The states m and v are kept in fp32, or in 8 bits with an fp32
  * scale for each 128 consecutive values: m as e4m3 (its scale is max |m| times
- * the fp32 nearest 1 / 448), v as e5m2 (max v times that nearest 1 / 57344).  An 8-bit state rounds to one of its two
- * neighbouring codes at random, up with the probability that keeps its mean,
- * because a step moves v by a thousandth and a code by an eighth: rounded to
- * the nearest, v would stand still.  v above 0 never becomes a code of 0
- * (it takes the smallest one), so that a step stays bounded.  The weights'
- * update comes from m and v before that rounding.
+ * the fp32 nearest 1 / 448), v as e5m2 (max v times that nearest 1 / 57344).
+ * An 8-bit state rounds to one of its two neighbouring codes at random, up with
+ * the probability that keeps its mean, because a step moves v by a thousandth
+ * and a code by an eighth: rounded to the nearest, v would stand still.  v above
+ * 0 never becomes a code of 0 (it takes the smallest one), so that a step stays
+ * bounded, unless its scale is 0 itself: a block whose largest v is below 2^-134.
+ * The weights' update comes from m and v before that rounding.
  *
  * The random numbers follow from the seed, the step, the tensor's number in
  * the call and the value's number in the tensor alone, so the same call gives

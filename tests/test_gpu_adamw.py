@@ -350,6 +350,7 @@ def test_streams_and_refusals(torch, moe):
     refused(ValueError, step=torch.tensor([1], device="cuda"))                   # 64 bits
     refused(ValueError, lr=torch.tensor([1.0, 2.0], device="cuda"))
     refused(ValueError, step=1 << 31)
+    refused(TypeError, step=1.5)
     refused(MoeError, step=0)
     refused(MoeError, betas=(1.0, 0.9))
     refused(MoeError, lr=float("nan"))
