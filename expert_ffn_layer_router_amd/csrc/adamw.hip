@@ -1,10 +1,10 @@
 // AdamW over many tensors (moe_optim.h): C entry point and kernel.
 //
 // Bound by memory: each value's weight, gradient and states pass once.  A block
-// of threads takes kChunk consecutive values of one tensor, 8 a thread at a
-// time; the tensors of a launch and where their chunks begin stand in the
-// kernel's arguments, so that one launch serves up to kTensors tensors of the
-// same types and nothing is copied to the device before it.
+// of threads takes kChunk consecutive values of one tensor, 8 a thread; the
+// tensors of a launch and where their chunks begin stand in the kernel's
+// arguments, so that one launch serves up to kTensors tensors of the same types
+// and nothing is copied to the device before it.
 //
 // 8-bit states have a scale for each 128 values, which 16 neighbouring lanes
 // hold.  A state x with scale s is coded as sign(x) n 2^e, where 2^e is the
@@ -12,15 +12,15 @@
 // random fraction of 2^16: n is the next whole number up with the probability
 // that |x| / (s 2^e) lies above the one below.
 //
-// Measured on one tensor of 2^28 values: fp32 weights and states 1408 us, 5.34
-// TB/s of what has to pass (a copy reaches 4.9); bf16 weights with fp32 ones
-// beside them 1419 us, 5.30 TB/s, with 8-bit states 818 us, 5.29 TB/s.  bf16
-// weights with 8-bit states alone, 10 bytes a value, take 550 us, 4.95 TB/s:
-// there the arithmetic counts, and with quotients and roots by the compiler's
-// exact divisions and the codes rounded by ordinary instructions it took 719 us.
-// 4096 values a block: with 2048 the memory-bound forms take 1% to 3% less and
-// the last one 2% more (a block works the step's numbers out once), with 16384
-// the former 2% to 5% more.  Stores past the caches change nothing.
+// Measured on one tensor of 2^28 values: fp32 weights and states 1390 us, 5.4 TB/s
+// of what has to pass (a copy reaches 4.9); bf16 weights with fp32 ones beside
+// them 1404 us, 5.35 TB/s, with 8-bit states 804 us, 5.4 TB/s.  bf16 weights with
+// 8-bit states alone, 10 bytes a value, 500 us, 5.4 TB/s; there the arithmetic
+// counts: by the compiler's exact divisions and roots, and with ordinary
+// instructions rounding the codes, 719 us; with two passes of 8 values a thread
+// and the step's numbers worked out by every block, not by the host, 550.  4096
+// values a block in two passes: 524 us, 1% to 3% more for the others; blocks of
+// 128 and of 512 threads, and stores past the caches, change nothing.
 #include <algorithm>
 #include <cmath>
 #include <vector>
@@ -34,7 +34,7 @@ namespace moe {
 namespace {
 
 constexpr int kStateBlock = 128;  // values that share a scale
-constexpr int kThreads = 256, kChunk = 4096;
+constexpr int kThreads = 256, kChunk = kThreads * 8;
 constexpr int kTensors = 36;
 
 struct AdamTensor {
@@ -47,17 +47,6 @@ struct AdamTensor {
   int32_t number;  // in the call
   uint32_t first;  // the first of its chunks
 };
-struct AdamArgs {
-  double lr, beta1, beta2, weight_decay;
-  float eps, grad_scale;
-  uint64_t seed;
-  int32_t step, tensors;
-  const float *device_lr, *device_grad_scale;
-  const int32_t* device_step;
-  AdamTensor t[kTensors];
-};
-static_assert(sizeof(AdamArgs) <= 4096 - 256, "kernel arguments");
-
 // What all values of a step share.
 struct Numbers {
   float b1, c1, b2, c2;  // beta, 1 - beta
@@ -65,7 +54,29 @@ struct Numbers {
   float rate;            // lr / (1 - beta1^t)
   float root;            // 1 / sqrt(1 - beta2^t)
   float eps, grad_scale;
+  uint32_t key;  // of seed and step
 };
+struct AdamArgs {
+  double lr, beta1, beta2, weight_decay;
+  float eps, grad_scale;
+  uint64_t seed;
+  int32_t step, tensors;
+  const float *device_lr, *device_grad_scale;
+  const int32_t* device_step;
+  Numbers numbers;  // without numbers on the device
+  AdamTensor t[kTensors];
+};
+static_assert(sizeof(AdamArgs) <= 4096 - 256, "kernel arguments");
+
+// The halves of x c, XORed; twice of it, with a key, makes a value's draw.
+__host__ __device__ __forceinline__ uint32_t fold(uint32_t x, uint32_t c) {
+  const uint64_t p = (uint64_t)x * c;
+  return (uint32_t)(p >> 32) ^ (uint32_t)p;
+}
+__host__ __device__ __forceinline__ uint32_t mix(uint32_t x, uint32_t key) {
+  return fold(fold(x ^ key, 0x9E3779B9u) + key, 0xBB67AE85u);
+}
+
 // beta^t by squaring, which takes few steps and the same ones everywhere.
 __host__ __device__ inline double power(double b, uint32_t t) {
   double r = 1.0;
@@ -75,9 +86,11 @@ __host__ __device__ inline double power(double b, uint32_t t) {
   }
   return r;
 }
-__device__ __forceinline__ Numbers numbers_of(const AdamArgs& a, int step) {
+// The same operations on the host and on the device: a step with its numbers in
+// device memory gives the bits of one that was given them.
+__host__ __device__ inline Numbers numbers_of(const AdamArgs& a, double lr, float grad_scale, int step) {
+#pragma clang fp contract(off)
   Numbers n;
-  const double lr = a.device_lr ? (double)*a.device_lr : a.lr;
   n.b1 = (float)a.beta1;
   n.c1 = (float)(1.0 - a.beta1);
   n.b2 = (float)a.beta2;
@@ -86,15 +99,11 @@ __device__ __forceinline__ Numbers numbers_of(const AdamArgs& a, int step) {
   n.rate = (float)(lr / (1.0 - power(a.beta1, step)));
   n.root = (float)(1.0 / sqrt(1.0 - power(a.beta2, step)));
   n.eps = a.eps;
-  n.grad_scale = a.device_grad_scale ? *a.device_grad_scale : a.grad_scale;
+  n.grad_scale = grad_scale;
+  n.key = mix((uint32_t)step, mix((uint32_t)(a.seed >> 32), (uint32_t)a.seed));
   return n;
 }
-
-// The halves of x c, XORed; twice of it, with a key, makes a value's draw.
-__device__ __forceinline__ uint32_t fold(uint32_t x, uint32_t c) { return __umulhi(x, c) ^ (x * c); }
-__device__ __forceinline__ uint32_t mix(uint32_t x, uint32_t key) {
-  return fold(fold(x ^ key, 0x9E3779B9u) + key, 0xBB67AE85u);
-}
+__host__ __device__ inline bool on_device(const AdamArgs& a) { return a.device_lr || a.device_grad_scale || a.device_step; }
 
 // The largest of 16 lanes, in each of them.
 __device__ __forceinline__ uint32_t max16(uint32_t v) {
@@ -234,111 +243,113 @@ __device__ __forceinline__ bool plain_roots(const Numbers& n) { return n.eps >= 
 template <typename P, typename G, bool MASTER, bool CODES>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs a) {
 #pragma clang fp contract(off)
-  int i = 0;  // the chunk's tensor: the last that begins at or before it
+  const uint32_t chunk = blockIdx.y * gridDim.x + blockIdx.x;
+  int i = 0;  // its tensor: the last that begins at or before it
   for (int past = a.tensors; past - i > 1;) {
     const int mid = (i + past) / 2;
-    if (a.t[mid].first <= blockIdx.x)
+    if (a.t[mid].first <= chunk)
       i = mid;
     else
       past = mid;
   }
   const AdamTensor& t = a.t[i];
-  const int64_t begin = (int64_t)(blockIdx.x - t.first) * kChunk;
-  const int step = a.device_step ? max(*a.device_step, 1) : a.step;
-  const Numbers n = numbers_of(a, step);
-  uint32_t key = 0;
-  if (CODES) {
-    key = mix((uint32_t)(a.seed >> 32), (uint32_t)a.seed);
-    key = mix((uint32_t)step, key);
-    key = mix((uint32_t)t.number, key);
-    key = mix((uint32_t)(begin >> 32), key);  // a chunk does not cross a multiple of 2^32
-  }
+  const int64_t begin = (int64_t)(chunk - t.first) * kChunk;
+  const Numbers n = !on_device(a) ? a.numbers
+                                  : numbers_of(a, a.device_lr ? (double)*a.device_lr : a.lr,
+                                               a.device_grad_scale ? *a.device_grad_scale : a.grad_scale,
+                                               a.device_step ? max(*a.device_step, 1) : a.step);
+  // (a chunk does not cross a multiple of 2^32)
+  const uint32_t key = mix((uint32_t)(begin >> 32), mix((uint32_t)t.number, n.key));
   P* param = (P*)t.param;
   const G* grad = (const G*)t.grad;
-  for (int64_t at = begin + threadIdx.x * 8; at < begin + kChunk; at += kThreads * 8) {
-    const int left = (int)min((int64_t)8, t.count - at);
-    // 16 lanes share a scale: they leave together
-    if (t.count <= at / kStateBlock * kStateBlock) break;
-    float p[8] = {}, g[8] = {}, m[8] = {}, v[8] = {};
-    if (left > 0) {
-      load8(grad + at, left, g);
-      if (MASTER)
-        load8(t.master + at, left, p);
-      else
-        load8(param + at, left, p);
-      if (CODES) {
-        const u32x2 cm = load_codes((const uint8_t*)t.m + at, left), cv = load_codes((const uint8_t*)t.v + at, left);
-        const float sm = t.m_scale[at / kStateBlock], sv = t.v_scale[at / kStateBlock];
-        E4M3::wide(cm[0], m);
-        E4M3::wide(cm[1], m + 4);
-        E5M2::wide(cv[0], v);
-        E5M2::wide(cv[1], v + 4);
+  const int64_t at = begin + threadIdx.x * 8;
+  const int left = (int)min((int64_t)8, t.count - at);
+  // 16 lanes share a scale: they leave together
+  if (t.count <= at / kStateBlock * kStateBlock) return;
+  float p[8] = {}, g[8] = {}, m[8] = {}, v[8] = {};
+  if (left > 0) {
+    load8(grad + at, left, g);
+    if (MASTER)
+      load8(t.master + at, left, p);
+    else
+      load8(param + at, left, p);
+    if (CODES) {
+      const u32x2 cm = load_codes((const uint8_t*)t.m + at, left), cv = load_codes((const uint8_t*)t.v + at, left);
+      const float sm = t.m_scale[at / kStateBlock], sv = t.v_scale[at / kStateBlock];
+      E4M3::wide(cm[0], m);
+      E4M3::wide(cm[1], m + 4);
+      E5M2::wide(cv[0], v);
+      E5M2::wide(cv[1], v + 4);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m[e] *= sm, v[e] *= sv;
-        if (left < 8) {
+      for (int e = 0; e < 8; ++e) m[e] *= sm, v[e] *= sv;
+      if (left < 8) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e >= left) m[e] = v[e] = 0.0f;
-        }
-      } else {
-        load8((const float*)t.m + at, left, m);
-        load8((const float*)t.v + at, left, v);
+        for (int e = 0; e < 8; ++e)
+          if (e >= left) m[e] = v[e] = 0.0f;
       }
+    } else {
+      load8((const float*)t.m + at, left, m);
+      load8((const float*)t.v + at, left, v);
     }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float gs = g[e] * n.grad_scale;
+    m[e] = m[e] * n.b1 + gs * n.c1;
+    v[e] = v[e] * n.b2 + (gs * gs) * n.c2;
+  }
+  if (plain_roots(n)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      p[e] = fmaf(-n.rate * m[e], __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_sqrtf(v[e]), n.root, n.eps)), p[e] * n.keep);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = p[e] * n.keep - n.rate * m[e] / (sqrtf(v[e]) * n.root + n.eps);
+  }
+  if (left > 0) {
+    if (MASTER) store8(t.master + at, left, p);
+    store8(param + at, left, p);
+  }
+  if (CODES) {
+    uint32_t um[8], uv[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float gs = g[e] * n.grad_scale;
-      m[e] = m[e] * n.b1 + gs * n.c1;
-      v[e] = v[e] * n.b2 + (gs * gs) * n.c2;
+      const uint32_t d = mix((uint32_t)at + e, key);
+      um[e] = d << 16;
+      uv[e] = d & 0xFFFF0000u;
     }
-    if (plain_roots(n)) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        p[e] = fmaf(-n.rate * m[e], __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_sqrtf(v[e]), n.root, n.eps)), p[e] * n.keep);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) p[e] = p[e] * n.keep - n.rate * m[e] / (sqrtf(v[e]) * n.root + n.eps);
-    }
+    float sm, sv;
+    const u32x2 cm = code8<E4M3, false>(m, um, sm), cv = code8<E5M2, true>(v, uv, sv);
     if (left > 0) {
-      if (MASTER) store8(t.master + at, left, p);
-      store8(param + at, left, p);
+      store_codes((uint8_t*)t.m + at, left, cm);
+      store_codes((uint8_t*)t.v + at, left, cv);
     }
-    if (CODES) {
-      uint32_t um[8], uv[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t d = mix((uint32_t)at + e, key);
-        um[e] = d << 16;
-        uv[e] = d & 0xFFFF0000u;
-      }
-      float sm, sv;
-      const u32x2 cm = code8<E4M3, false>(m, um, sm), cv = code8<E5M2, true>(v, uv, sv);
-      if (left > 0) {
-        store_codes((uint8_t*)t.m + at, left, cm);
-        store_codes((uint8_t*)t.v + at, left, cv);
-      }
-      if ((threadIdx.x & 15) == 0) {
-        t.m_scale[at / kStateBlock] = sm;
-        t.v_scale[at / kStateBlock] = sv;
-      }
-    } else if (left > 0) {
-      store8((float*)t.m + at, left, m);
-      store8((float*)t.v + at, left, v);
+    if ((threadIdx.x & 15) == 0) {
+      t.m_scale[at / kStateBlock] = sm;
+      t.v_scale[at / kStateBlock] = sv;
     }
+  } else if (left > 0) {
+    store8((float*)t.m + at, left, m);
+    store8((float*)t.v + at, left, v);
   }
 }
 
-// A launch has at most 2^32 threads.
-constexpr int64_t kMaxChunks = ((int64_t)1 << 32) / kThreads - 1;
+constexpr int64_t kMaxChunks = (int64_t)1 << 24;  // of a launch
 constexpr int64_t kMaxCount = (int64_t)1 << 35;
 static_assert(kMaxCount / kChunk <= kMaxChunks, "a tensor fits a launch");
+// A grid has fewer than 2^32 threads in x.  The blocks that y adds behind the
+// last chunk find nothing.
+dim3 grid_of(int64_t chunks) {
+  const int64_t x = std::min<int64_t>(chunks, 1 << 20);
+  return dim3((unsigned)x, (unsigned)((chunks + x - 1) / x));
+}
 
 template <typename P, typename G, bool MASTER>
 void launch(const AdamArgs& a, int64_t chunks, bool codes, hipStream_t s) {
   if (codes)
-    adamw_kernel<P, G, MASTER, true><<<(unsigned)chunks, kThreads, 0, s>>>(a);
+    adamw_kernel<P, G, MASTER, true><<<grid_of(chunks), kThreads, 0, s>>>(a);
   else
-    adamw_kernel<P, G, MASTER, false><<<(unsigned)chunks, kThreads, 0, s>>>(a);
+    adamw_kernel<P, G, MASTER, false><<<grid_of(chunks), kThreads, 0, s>>>(a);
 }
 template <typename P>
 void launch_half(const AdamArgs& a, int64_t chunks, bool wide_grad, bool master, bool codes, hipStream_t s) {
@@ -462,6 +473,7 @@ MOE_EXPORT moe_status moe_adamw_step(const moe_adamw* n, int32_t count, const mo
   a.device_lr = n->device_lr;
   a.device_grad_scale = n->device_grad_scale;
   a.device_step = n->device_step;
+  if (!on_device(a)) a.numbers = numbers_of(a, a.lr, a.grad_scale, a.step);
   // tensors of the same types share launches, in their order
   for (int type = MOE_TYPE_BF16; type <= MOE_TYPE_FP32; ++type)
     for (int kind = 0; kind < (type == MOE_TYPE_FP32 ? 1 : 4); ++kind) {
