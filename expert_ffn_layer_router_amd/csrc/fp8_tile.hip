@@ -48,8 +48,10 @@ __device__ __forceinline__ u32x2 read_transposed8(lds_char* __restrict p) {
 // group's last tile with its rows spread over all waves and only as many row
 // blocks as it has (its zeros cost little power, and power is what there is);
 // units dealt to the XCDs round by round, for the same reason; staggered starts;
-// four stages of 128 x 128 ahead where tiles are few (copies, not their latency,
-// bound a stage: 0.6 us).
+// four stages of 128 x 128 ahead where tiles are few (a stage takes 0.6 us either
+// way); 64 x 64 blocks of one wave there (300 rows, 4096 and 4096, input gradient:
+// 26.5 -> 35.5 us); splitting their contraction earlier than ops_api.hip's rule
+// (300 rows over 5, 1008 and 1424: 20.2 -> 22.3 us with the join).
 template <Pass PASS, Result RES, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp8_tile_kernel(Fp8Args a) {
   constexpr int NW = WM * WN, THREADS = 64 * NW;
