@@ -114,11 +114,12 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
         pointers = [_column(c, "params", params, shapes, None), _column(c, "grads", grads, shapes, None)]
         if master is None:
             pointers.append([0] * count)
+            wide = ()
         else:
             given = [i for i in range(count) if master[i] is not None]
-            wide = _column(c, "master", [master[i] for i in given], [shapes[i] for i in given], float32)
+            wide = [master[i] for i in given]
             pointers.append([0] * count)
-            for i, at in zip(given, wide):
+            for i, at in zip(given, _column(c, "master", wide, [shapes[i] for i in given], float32)):
                 pointers[2][i] = at
         pointers += [_column(c, "m", m, shapes, m_type), _column(c, "v", v, shapes, v_type)]
         values = list(map(env.torch.Tensor.numel, params))
@@ -133,5 +134,5 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
         # would take longer than the checks
         table = _words(9 * count).pack(*chain.from_iterable(zip(*pointers, values, kinds)))
         _lib.check(c.lib.moe_adamw_step(ctypes.byref(n), count, table, c.stream))
-    # autograd then refuses a backward pass through what the step has overwritten (inference tensors take part in none)
-    env.torch.autograd.graph.increment_version([p for p in params if not p.is_inference()])
+    # autograd then refuses a backward pass through what the step has overwritten
+    env.torch.autograd.graph.increment_version([*params, *wide, *m, *v, *(m_scale or ()), *(v_scale or ())])
