@@ -104,12 +104,8 @@ def quantize_blocks(x, tiles=False, codes=None, scale=None, stream=None):
     shape = _scale_shape(x.shape)
     with _Call(x, stream) as c:
         px = c.plain("x", x, x.shape, x.dtype)
-        if codes is None:
-            codes = c.empty(x.shape, e4m3)
-        if scale is None:
-            scale = c.empty(shape, c.env.float32)
-        pc = c.plain("codes", codes, x.shape, e4m3)
-        ps = c.plain("scale", scale, shape, c.env.float32)
+        codes, pc = c.plain_result("codes", codes, x.shape, e4m3)
+        scale, ps = c.plain_result("scale", scale, shape, c.env.float32)
         _lib.check(c.lib.moe_quantize_tiles(matrices, n, k, _type(x.dtype), px, pc, ps, c.stream))
     return codes, scale
 

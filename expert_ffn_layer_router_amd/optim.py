@@ -134,5 +134,4 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
         # would take longer than the checks
         table = _words(9 * count).pack(*chain.from_iterable(zip(*pointers, values, kinds)))
         _lib.check(c.lib.moe_adamw_step(ctypes.byref(n), count, table, c.stream))
-    # autograd then refuses a backward pass through what the step has overwritten
-    env.torch.autograd.graph.increment_version([*params, *wide, *m, *v, *(m_scale or ()), *(v_scale or ())])
+    env.overwritten([*params, *wide, *m, *v, *(m_scale or ()), *(v_scale or ())])

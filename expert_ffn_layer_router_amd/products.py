@@ -15,7 +15,9 @@ not given there; with `out` and `workspace` given it allocates nothing.  On
 another stream than the current one the caller orders the call after what
 wrote its inputs; their memory is kept from reuse until it is done.  Nothing is
 recorded for autograd: the backward calls are the caller's, and with gradients
-enabled a tensor that requires one is refused (its result would be cut off)."""
+enabled a tensor that requires one is refused (its result would be cut off).
+A given result counts as modified in place: autograd refuses a backward pass
+through what it held before."""
 
 from __future__ import annotations
 
@@ -43,6 +45,8 @@ class _Torch:
         # the raw handle without a Stream object around it (2 us less), where this torch has it
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                                   lambda index: torch.cuda.current_stream(index).cuda_stream)
+        # autograd then refuses a backward pass through what stood in a tensor (or a list of them) before the call
+        self.overwritten = torch.autograd.graph.increment_version
         self.lib = _lib.load()
 
 
@@ -192,7 +196,18 @@ class _Call:
         if out is None:
             out = self.empty((rows, width), dtype)
             return out, out.data_ptr(), width
-        return (out, *self.rows(name, out, rows, width, dtype))
+        pointer, stride = self.rows(name, out, rows, width, dtype)
+        self.env.overwritten(out)
+        return out, pointer, stride
+
+    def plain_result(self, name, out, shape, dtype):
+        """(a contiguous result, its pointer)."""
+        if out is None:
+            out = self.empty(shape, dtype)
+            return out, out.data_ptr()
+        pointer = self.plain(name, out, shape, dtype)
+        self.env.overwritten(out)
+        return out, pointer
 
 
 def _weights(w, gated):
@@ -222,9 +237,7 @@ def quantize_rows(x, codes=None, scale=None, stream=None):
     with _Call(x, stream) as c:
         px, ldx = c.rows("x", x, rows, k, x.dtype)
         codes, pc, ldc = c.result("codes", codes, rows, k, c.env.int8)
-        if scale is None:
-            scale = c.empty(rows, c.env.float32)
-        ps = c.plain("scale", scale, (rows,), c.env.float32)
+        scale, ps = c.plain_result("scale", scale, (rows,), c.env.float32)
         _lib.check(c.lib.moe_quantize_rows(rows, k, _type(x.dtype), px, ldx, pc, ldc, ps, c.stream))
     return codes, scale
 
@@ -329,9 +342,7 @@ def _backward(name, dy, gate_up, x, w, offsets, activation, need_dx, need_dw, dx
         if need_dx:
             dx, pdx, lddx = c.result("dx", dx, rows, k, dtype)
         if need_dw:
-            if dw is None:
-                dw = c.empty(w_shape, dw_dtype or dtype)
-            pdw = c.plain("dw", dw, w_shape, dw_dtype or dw.dtype)
+            dw, pdw = c.plain_result("dw", dw, w_shape, dw_dtype or (dtype if dw is None else dw.dtype))
         ws, ws_bytes, _alive = c.workspace(workspace, need)
         dw_type = _type(dw.dtype) if need_dw else shape.type
         head = (ctypes.byref(shape), py, ldy)

@@ -58,3 +58,80 @@ def test_inference_tensors_have_no_version(torch, moe):
         master = param.float()
         moe.adamw_step([param], [torch.ones_like(param)], step=1, lr=0.1, master=[master], **states)
         assert torch.equal(param, master.bfloat16()) and (param < 1).all()
+        codes = torch.empty(4, 128, device="cuda", dtype=torch.float8_e4m3fn)
+        moe.quantize_blocks(torch.ones(4, 128, device="cuda").half(), codes=codes)
+        assert (codes.float() == 448).all()
+
+
+def calls(torch, moe):
+    """(name, the tensors given for results, the other tensors, the call) of every operator that takes results."""
+    bf16, e4m3, i8 = torch.bfloat16, torch.float8_e4m3fn, torch.int8
+
+    def make(dtype, *shape):
+        return torch.zeros(shape, dtype=dtype, device="cuda")
+
+    x, dy, gu, w, gw = (make(bf16, *s) for s in ((4, 64), (4, 32), (4, 64), (32, 64), (64, 64)))
+    codes, scale = make(e4m3, 4, 64), make(torch.float32, 1, 4)
+    wq, ws = make(e4m3, 32, 64), make(torch.float32, 1, 1)
+    gq, gs = make(e4m3, 2, 32, 64), make(torch.float32, 2, 1, 1)
+    dq = make(e4m3, 4, 32)
+    c8, s8, w8, ws8, g8, gs8 = (make(i8, 4, 64), make(torch.float32, 4), make(i8, 32, 64), make(torch.float32, 32),
+                                make(i8, 64, 64), make(torch.float32, 64))
+    y, h, k, dx, sl, dw, gdw = (make(bf16, *s) for s in ((4, 32), (4, 32), (4, 64), (4, 64), (4, 64), (32, 64), (64, 64)))
+    c, s, t, ts = make(e4m3, 4, 64), make(torch.float32, 1, 4), make(e4m3, 32, 64), make(torch.float32, 1, 1)
+    r, rs = make(i8, 4, 64), make(torch.float32, 4)
+    return [
+        ("quantize_blocks", [c, s], [x], lambda: moe.quantize_blocks(x, codes=c, scale=s)),
+        ("quantize_blocks tiles", [t, ts], [w], lambda: moe.quantize_blocks(w, tiles=True, codes=t, scale=ts)),
+        ("fp8_product", [y], [codes, scale, wq, ws], lambda: moe.fp8_product(codes, scale, wq, ws, out=y)),
+        ("fp8_gated", [h, k], [codes, scale, gq, gs], lambda: moe.fp8_gated(codes, scale, gq, gs, out=h, gate_up=k)),
+        ("fp8_product_backward", [dx], [dq, scale, wq, ws], lambda: moe.fp8_product_backward(dq, scale, wq, ws, dx=dx)),
+        ("fp8_gated_backward", [dx, sl], [dy, gu, gq, gs],
+         lambda: moe.fp8_gated_backward(dy, gu, gq, gs, dx=dx, slopes=sl)),
+        ("quantize_rows", [r, rs], [x], lambda: moe.quantize_rows(x, codes=r, scale=rs)),
+        ("int8_product", [y], [c8, s8, w8, ws8], lambda: moe.int8_product(c8, s8, w8, ws8, out=y)),
+        ("int8_gated", [h], [c8, s8, g8, gs8], lambda: moe.int8_gated(c8, s8, g8, gs8, out=h)),
+        ("expert_product", [y], [x, w], lambda: moe.expert_product(x, w, out=y)),
+        ("expert_product_backward", [dx, dw], [dy, x, w], lambda: moe.expert_product_backward(dy, x, w, dx=dx, dw=dw)),
+        ("gated_product", [h, k], [x, gw], lambda: moe.gated_product(x, gw, out=h, gate_up=k)),
+        ("gated_product_backward", [dx, gdw], [dy, gu, x, gw],
+         lambda: moe.gated_product_backward(dy, gu, x, gw, dx=dx, dw=gdw)),
+    ]
+
+
+def test_given_results_are_raised(torch, moe):
+    for name, given, others, call in calls(torch, moe):
+        assert raised(call, given) == [True] * len(given), name
+        assert not any(raised(call, others)), name
+
+
+def test_a_kept_gate_up_that_a_second_forward_overwrites(torch, moe):
+    """One buffer for the kept (g, u) of two forward passes: the first one's backward pass is refused."""
+    class Gated(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w, w_scale, gate_up):
+            h, gate_up = moe.fp8_gated(*moe.quantize_blocks(x), w, w_scale, gate_up=gate_up)
+            ctx.save_for_backward(gate_up, w, w_scale)
+            return h
+
+        @staticmethod
+        def backward(ctx, dh):
+            gate_up, w, w_scale = ctx.saved_tensors
+            return moe.fp8_gated_backward(dh, gate_up, w, w_scale, need_slopes=False)[0], None, None, None
+
+    gen = torch.Generator(device="cuda").manual_seed(0)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=gen, device="cuda").bfloat16()
+
+    w, w_scale = moe.quantize_blocks(normal(2, 32, 64), tiles=True)
+    x = [normal(4, 64).requires_grad_() for _ in range(2)]
+    buffer = torch.empty(4, 64, dtype=torch.bfloat16, device="cuda")
+    first, second = (Gated.apply(v, w, w_scale, buffer) for v in x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        first.backward(torch.ones_like(first))
+    second.backward(torch.ones_like(second))
+    own = torch.empty_like(buffer)
+    alone = Gated.apply(x[0], w, w_scale, own)
+    alone.backward(torch.ones_like(alone))
+    assert x[0].grad.isfinite().all() and x[1].grad.isfinite().all()
