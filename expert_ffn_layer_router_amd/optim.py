@@ -18,7 +18,7 @@ from itertools import chain
 from operator import attrgetter, index
 
 from . import _lib
-from .products import _Call, _type
+from .products import _Call, _env, _type
 
 _dtype_of, _shape_of, _tracked = attrgetter("dtype"), attrgetter("shape"), attrgetter("requires_grad")
 BLOCK = 128  # values of an 8-bit state that share a scale
@@ -43,6 +43,12 @@ def adamw_states(params, bits=32):
     return states
 
 
+@lru_cache(maxsize=2)
+def _tensor_types(none):
+    torch = _env().torch
+    return frozenset((torch.Tensor, torch.nn.Parameter) + ((type(None),) if none else ()))
+
+
 def _lists(**lists):
     length = None
     for name, tensors in lists.items():
@@ -54,6 +60,12 @@ def _lists(**lists):
             length = len(tensors)
         if len(tensors) != length:
             raise ValueError(f"{name} has {len(tensors)} tensors, params {length}")
+        # (one pass by type where all is right; an entry of master may be None)
+        if not _tensor_types(name == "master").issuperset(map(type, tensors)):
+            tensor = _env().torch.Tensor
+            for i, t in enumerate(tensors):
+                if not isinstance(t, tensor) and not (name == "master" and t is None):
+                    raise ValueError(f"{name}[{i}] must be a tensor, not {t!r}")
 
 
 @lru_cache(maxsize=64)
