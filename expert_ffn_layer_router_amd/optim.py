@@ -91,7 +91,8 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
     m_scale and v_scale (adamw_states).  master, for params in 16 bits: their values in fp32, which the step updates
     and params then are the rounding of; an entry may be None.  step counts from 1.  Gradients are multiplied by
     grad_scale first (clipping, loss scales).  8-bit states round at random, by numbers that follow from seed, step
-    and each value's place.  step (int32), lr and grad_scale (fp32) may be tensors of one value on the device: a
+    and each value's place in the lists: calls of one step (groups of parameters) draw the same numbers unless each has a
+    seed of its own.  step (int32), lr and grad_scale (fp32) may be tensors of one value on the device: a
     captured call then reads them at each replay."""
     _lists(params=params, grads=grads, m=m, v=v, master=master, m_scale=m_scale, v_scale=v_scale)
     if (m_scale is None) != (v_scale is None):
