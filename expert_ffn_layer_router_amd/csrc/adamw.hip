@@ -14,13 +14,18 @@
 //
 // Measured on one tensor of 2^28 values: fp32 weights and states 1390 us, 5.4 TB/s
 // of what has to pass (a copy reaches 4.9); bf16 weights with fp32 ones beside
-// them 1404 us, 5.35 TB/s, with 8-bit states 804 us, 5.4 TB/s.  bf16 weights with
-// 8-bit states alone, 10 bytes a value, 500 us, 5.4 TB/s; there the arithmetic
-// counts: by the compiler's exact divisions and roots, and with ordinary
-// instructions rounding the codes, 719 us; with two passes of 8 values a thread
-// and the step's numbers worked out by every block, not by the host, 550.  4096
-// values a block in two passes: 524 us, 1% to 3% more for the others; blocks of
+// them 1402 us, 5.35 TB/s, with 8-bit states 793 us, 5.45 TB/s.  bf16 weights with
+// 8-bit states alone, 10 bytes a value, 472 to 500 us by box, 5.4 to 5.7 TB/s; there
+// the arithmetic counts: by the compiler's exact divisions and roots, and with
+// ordinary instructions rounding the codes, 719 us; with two passes of 8 values a
+// thread and the step's numbers worked out by every block, not by the host, 550.
+// 4096 values a block in two passes: 524 us, 1% to 3% more for the others; blocks of
 // 128 and of 512 threads, and stores past the caches, change nothing.
+//
+// A step with numbers on the device has every thread work all of them out, in 64
+// bits: bf16 weights with 8-bit states 577 us where the host's numbers take 472 (623
+// at a step past 10^6, whose powers are longer), with fp32 ones beside them 801
+// (793; 844), with fp32 states 1406 (1402), all in fp32 1383 (1393).
 #include <algorithm>
 #include <cmath>
 #include <vector>

@@ -17,7 +17,7 @@
 // All three kernels are bound by memory: rows 8192 x 14336 take 66 to 80 us (4.5
 // to 5.4 TB/s, by how much of them the last-level cache still holds), 16 matrices
 // of 14336 x 4096 528 us (5.3 TB/s; a copy 4.9), the slopes of 4096 x 14336 with
-// their 16-bit copy 108 us (6.5 TB/s).
+// their 16-bit copy 111 us (6.4 TB/s).
 #include <type_traits>
 
 #include "fp8_device.h"

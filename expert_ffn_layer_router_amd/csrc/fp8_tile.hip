@@ -29,12 +29,12 @@ __device__ __forceinline__ u32x2 read_transposed8(lds_char* __restrict p) {
 //  - A lane of the result holds four columns of one row, so a row block's scales
 //    are one register; a lane loads one row's in 64 and the lanes exchange them.
 //
-// What bounds it: power, and behind it the matrix cores' feeding.  At 8192^3 with
-// random codes 432 us, 2545 TFLOP/s forward, 2510 input gradient and gated (a
-// large library product of plain 8-bit floats, without scales: 2630; integer
-// codes by this library, 2840); with all codes zero, where nothing switches and
-// the clock stays up, 321 us: the matrix cores are busy 66% of the cycles.
-// Registers alone, the products reach 4350 TFLOP/s and with the FMAs 3650; the
+// What bounds it: the matrix cores' feeding (they are busy 66% of the cycles) and
+// the clock, which power lowers.  At 8192^3 with random codes 432 us, 2545
+// TFLOP/s forward, 2510 input gradient and gated (a large library product of
+// plain 8-bit floats, without scales: 2630; integer codes by this library, 2840);
+// with all codes zero, where nothing switches and the clock stays up, the same
+// launch takes 321 us.  Registers alone, the products reach 4350 TFLOP/s and with the FMAs 3650; the
 // FMAs cost 13% in the whole kernel too, the copies 25%, LDS reads 2%.  Each
 // step, timed at that size:
 //  - two buffers, copies and fragment reads after the barrier: 630 us;
@@ -43,11 +43,17 @@ __device__ __forceinline__ u32x2 read_transposed8(lds_char* __restrict p) {
 //  - one scale load in 64 lanes instead of one for every row block: 450;
 //  - the hand-over to the next stage half way, not before the last two row
 //    blocks, and five row fragments in registers, not four: 432.
+// Rows that a group's last tile has not cost two thirds of what its rows do: 256
+// tiles of 14336 contracted and 4096 columns take 213 us for 8 groups of 512 rows,
+// 187 of 384, 176 of 257; 64 groups' input gradient, 2048 columns of 4096, 158 for
+// 256 rows each, 223 for 257.
 // No gain: raised wave priority for the products; two tiles between the
 // schedule's fences; the last two row blocks together, for earlier Q reads; a
 // group's last tile with its rows spread over all waves and only as many row
-// blocks as it has (its zeros cost little power, and power is what there is);
-// units dealt to the XCDs round by round, for the same reason; staggered starts;
+// blocks as it has (the units stay as many: 4096 rows over 8 groups and 4096
+// columns are one round of 256 and 64 tiles in 4 parts, from which a unit that ends
+// early takes nothing away; a remainder of up to 128 rows counted as half a unit
+// would, which is not built); units dealt to the XCDs round by round; staggered starts;
 // four stages of 128 x 128 ahead where tiles are few (a stage takes 0.6 us either
 // way); 64 x 64 blocks of one wave there (300 rows, 4096 and 4096, input gradient:
 // 26.5 -> 35.5 us); splitting their contraction earlier than ops_api.hip's rule

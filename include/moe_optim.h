@@ -21,7 +21,8 @@
  * The random numbers follow from the seed, the step, the tensor's number in
  * the call and the value's number in the tensor alone, so the same call gives
  * the same bits, and two calls of one step (groups of parameters) draw the same
- * numbers unless each has a seed of its own.  With fold(x, c) = the two 32-bit halves of x c, XORed, and
+ * numbers unless each has a seed of its own.  With fold(x, c) = the two 32-bit
+ * halves of x c, XORed, and
  * mix(x, key) = fold(fold(x ^ key, 0x9E3779B9) + key, 0xBB67AE85):
  *   key = low(seed); key = mix(y, key) for y = high(seed), step, tensor,
  *   high(value);  draw = mix(low(value), key)
