@@ -44,9 +44,8 @@
  * seven products of 6 beside 448 x 448 are gone.  That is less than fp32, so
  * results are in 16 bits only.  Then sum += (scale * w_scale) * block, in fp32,
  * so that scale * w_scale has to stay in its range.  The same call gives the
- * same bits.  A scale that is NaN makes
- * NaN of every result that its block takes part in, and so does a code that
- * is NaN.
+ * same bits.  A scale that is NaN makes NaN of every result that its block takes
+ * part in, and so does a code that is NaN.
  */
 #ifndef MOE_FP8_H_
 #define MOE_FP8_H_
@@ -105,7 +104,9 @@ moe_status moe_fp8_product_backward(const moe_product *p, const uint8_t *codes, 
  * p->type, or is NULL.  Either of dx and slopes may be NULL (w and w_scale
  * are not needed without dx).  The codes come from (dg, du) before their
  * rounding to 16 bits, and have fp32 scales: in fp16 a slope past 65504 is
- * infinite in `slopes` and finite in dx. */
+ * infinite in `slopes` and finite in dx.  The activation is within some 2e-6 of
+ * itself, so a slope next to the middle of two codes may take either: 5 to 8 in
+ * a million do, 0.7e-4 to 1.6e-4 of the codes' norm. */
 moe_status moe_fp8_gated_backward(const moe_product *p, const uint16_t *dh, int64_t lddh, const uint16_t *gate_up,
                                   int64_t ldgate_up, const uint8_t *w, const float *w_scale, const int32_t *offsets,
                                   uint16_t *dx, int64_t lddx, uint16_t *slopes, int64_t ldslopes, void *workspace,
